@@ -594,6 +594,134 @@ ms_status mamba_probe_unit_throughput(int unit, void *scratch, double *ops_per_s
  */
 ms_status mamba_scan_fwd_noalloc(const ms_scan_args *args, void *stream);
 
+/* ---- Mamba-2 serving: packed sequences and states in slots -----------------
+ * A serving program runs requests of different lengths together. Their tokens
+ * are packed one behind the other: sequence s owns rows cu_seqlens[s] to
+ * cu_seqlens[s + 1] - 1 of every token tensor (cu_seqlens: nseq + 1
+ * non-decreasing int32 values in device memory; values outside [0, tokens] are
+ * taken as the nearer end). A sequence may be empty. Rows before the first and
+ * behind the last sequence are not read, nor written in the outputs.
+ *
+ * The requests' states live in a cache of `slots` entries: sequence s uses
+ * entry state_indices[s] (device int32; NULL = entry s). has_initial_state
+ * (device bytes, one per sequence; NULL = none): nonzero where the sequence
+ * continues from its entry's state, zero where it starts from zero. At the end
+ * the entry holds the state after the sequence's last token (for an empty
+ * sequence: the state it started from). `state` may be NULL: every sequence
+ * then starts from zero, none leaves a state, and state_indices and
+ * has_initial_state must be NULL.
+ *
+ * A sequence is SKIPPED when its index is negative, at least `slots`, or an
+ * earlier sequence of the call has the same one: its rows of the outputs and
+ * every cache entry are left as they were. A batch padded to a fixed size
+ * gives its empty places a negative index.
+ *
+ * The single-token calls are the same with one row per sequence, always
+ * continuing from the entry's state.
+ */
+
+/*
+ * Causal depthwise convolution over packed sequences, channels contiguous:
+ *   y[t, c] = act(bias[c] + sum_k weight[c, k] x[t - width + 1 + k, c])
+ * with the rows before the sequence's first token taken from its state (the
+ * last width - 1 inputs, oldest first) or zero. conv->silu: act = SiLU.
+ * The convolution in front of the Mamba-2 scan runs over x, B and C together.
+ *   x, y  : (tokens, channels), in_dtype, row strides given, channels contiguous
+ *   state : (slots, width - 1, channels) in_dtype, updated in place; entry and
+ *           row strides given. Unused (NULL) when width is 1.
+ * cu_seqlens NULL is the single-token form: tokens == nseq, sequence s is row s.
+ */
+typedef struct ms_conv_packed_args {
+    int64_t tokens, channels, nseq, slots;
+    int32_t in_dtype, reserved;                 /* reserved: 0 */
+    const void *x;      int64_t x_token_stride;
+    void *y;            int64_t y_token_stride;
+    void *state;        int64_t state_slot_stride, state_row_stride;
+    const int32_t *cu_seqlens;
+    const int32_t *state_indices;
+    const uint8_t *has_initial_state;           /* must be NULL in the single-token form */
+} ms_conv_packed_args;
+
+ms_status mamba_conv_packed_fwd(const ms_conv_packed_args *args, const ms_conv1d_args *conv, void *stream);
+
+/*
+ * One token per request through the Mamba-2 recurrence, states in slots:
+ *   x, z, y : (batch, nheads, headdim), dt : (batch, nheads),
+ *   B, C    : (batch, ngroups, dstate); batch strides given, inner axes contiguous
+ *   state   : (slots, nheads, headdim, dstate) float32, updated in place; slot
+ *             stride given, inner axes contiguous
+ * Any headdim up to 65535, dstate up to MS_SSD_UPDATE_MAX_DSTATE; in_dtype f32
+ * or bf16.
+ */
+#define MS_SSD_UPDATE_MAX_DSTATE 256
+typedef struct ms_ssd_update_args {
+    int64_t batch, nheads, ngroups, headdim, dstate, slots;
+    int32_t in_dtype, dt_softplus;
+    float *state;       int64_t state_slot_stride;
+    const void *x;      int64_t x_batch_stride;
+    const void *dt;     int64_t dt_batch_stride;
+    const void *B;      int64_t B_batch_stride;
+    const void *C;      int64_t C_batch_stride;
+    const void *z;      int64_t z_batch_stride;    /* z may be NULL */
+    void *y;            int64_t y_batch_stride;
+    const float *A;
+    const float *D;
+    const float *dt_bias;
+    const int32_t *state_indices;
+} ms_ssd_update_args;
+
+ms_status mamba_ssd_state_update(const ms_ssd_update_args *args, void *stream);
+
+/* ---- RMS norm before and after a block --------------------------------------
+ * Per row and group of group_size consecutive channels, in float32:
+ *   v = x,  v = x silu(z)                          if z and gate_first
+ *   v = residual + residual_scale v                if residual; residual_out = v
+ *   y = v rsqrt(mean_group(v^2) + eps) weight      (weight NULL: ones)
+ *   y = y silu(z)                                  if z and not gate_first
+ * The norm before a block takes the block's input out of the residual stream
+ * (residual, residual_scale); the norm after the Mamba-2 scan takes the gate
+ * (z, groups). x, z, y, dy: in_dtype; residual and residual_out:
+ * residual_dtype, which is in_dtype or MS_F32. Row strides given, channels
+ * contiguous. weight: (dim) float32.
+ */
+typedef struct ms_norm_args {
+    int64_t rows, dim, group_size;
+    int32_t in_dtype, residual_dtype;
+    float eps, residual_scale;
+    int32_t gate_first, reserved;                  /* gate_first: 0 or 1; reserved: 0 */
+    const void *x;           int64_t x_row_stride;
+    const void *z;           int64_t z_row_stride;             /* may be NULL */
+    const void *residual;    int64_t residual_row_stride;      /* may be NULL */
+    void *residual_out;      int64_t residual_out_row_stride;  /* given exactly when residual is */
+    void *y;                 int64_t y_row_stride;
+    const float *weight;
+} ms_norm_args;
+
+ms_status mamba_norm_fwd(const ms_norm_args *args, void *stream);
+
+/*
+ * Gradients of mamba_norm_fwd for the loss sum(y dy) + sum(residual_out
+ * dresidual_out). In `fwd`, y and residual are not used: residual_out says by
+ * being given whether the forward had a residual, and the sum is read from it
+ * as the forward stored it. x is then read only for a gate that comes first. dweight (dim) float32 may be NULL.
+ * dx and dz have in_dtype, dresidual and dresidual_out (NULL = zero)
+ * residual_dtype. dz is required with z, dresidual with residual_out. The
+ * sums over the rows are taken in a fixed order. The workspace (16-byte
+ * aligned) is needed for dweight only.
+ */
+typedef struct ms_norm_bwd_args {
+    const void *dy;             int64_t dy_row_stride;
+    const void *dresidual_out;  int64_t dresidual_out_row_stride;   /* may be NULL */
+    void *dx;                   int64_t dx_row_stride;
+    void *dz;                   int64_t dz_row_stride;
+    void *dresidual;            int64_t dresidual_row_stride;
+    float *dweight;
+} ms_norm_bwd_args;
+
+ms_status mamba_norm_bwd_workspace_size(const ms_norm_args *fwd, size_t *bytes);
+ms_status mamba_norm_bwd(const ms_norm_args *fwd, const ms_norm_bwd_args *bwd, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

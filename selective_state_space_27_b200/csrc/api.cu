@@ -721,4 +721,255 @@ ms_status mamba_ssd_fwd(const ms_ssd_args *a, void *workspace, size_t workspace_
     return MS_OK;
 }
 
+// ---- Mamba-2 serving operators and norms --------------------------------------
+
+static ms_status misaligned(const char *what) {
+    set_error("%s", what);
+    return MS_ERR_ALIGNMENT;
+}
+
+static ms_status unsupported(const char *what) {
+    set_error("%s", what);
+    return MS_ERR_UNSUPPORTED;
+}
+
+// Element size of an ms_dtype, 0 for an unknown one.
+static int dtype_bytes(int dtype) { return dtype == MS_F32 ? 4 : dtype == MS_BF16 ? 2 : 0; }
+
+// Rows of packed tensors and cache slots are counted in 32 bits on the device.
+static const int64_t kMaxRows = (int64_t(1) << 31) - 1;
+
+// The checks that the packed calls share: counts, the cache and its index table.
+static ms_status check_slots(int64_t nseq, int64_t slots, const void *state, const int32_t *idx,
+                             const uint8_t *has_init, bool need_state) {
+    if (nseq < 0 || slots < 0 || nseq > kMaxRows || slots > kMaxRows) return invalid("nseq or slots out of range");
+    if (!state && need_state && (idx || has_init))
+        return invalid("state_indices and has_initial_state need a state");
+    if (state && !idx && slots < nseq) return invalid("without state_indices there must be a slot for every sequence");
+    if (idx && !elem_aligned(idx, 4)) return misaligned("state_indices is not aligned to 4 bytes");
+    return MS_OK;
+}
+
+ms_status mamba_conv_packed_fwd(const ms_conv_packed_args *a, const ms_conv1d_args *c, void *stream) {
+    const CallRange range("mamba_conv_packed_fwd");
+    if (!a) return invalid("args is NULL");
+    ms_status st = check_conv(c);
+    if (st != MS_OK) return st;
+    const int eb = dtype_bytes(a->in_dtype);
+    if (!eb) return invalid("in_dtype");
+    if (a->reserved != 0) return invalid("reserved must be 0");
+    if (a->tokens < 0 || a->tokens > kMaxRows - 64 || a->channels <= 0 || a->channels > (int64_t(1) << 22))
+        return invalid("tokens must be in [0, 2^31 - 65] and channels in [1, 2^22]");
+    const bool stateful = a->state != nullptr && c->width > 1;
+    st = check_slots(a->nseq, a->slots, a->state, a->state_indices, a->has_initial_state, c->width > 1);
+    if (st != MS_OK) return st;
+    if (!a->cu_seqlens && (a->tokens != a->nseq || a->has_initial_state))
+        return invalid("single tokens: tokens must equal nseq and has_initial_state be NULL");
+    if (!a->cu_seqlens && c->width > 1 && !a->state) return invalid("single tokens need a state");
+    if (a->nseq > (int64_t(1) << 30)) return invalid("nseq above 2^30");
+    if (a->tokens > 0 && (!a->x || !a->y)) return invalid("x and y are required");
+    if (a->x_token_stride < 0 || a->y_token_stride < a->channels ||
+        (stateful && (a->state_slot_stride < 0 || a->state_row_stride < a->channels)))
+        return invalid("strides must be non-negative and those of y and the state rows cover the channels");
+    if (stateful && a->slots > 1 && a->state_slot_stride < a->state_row_stride * (c->width - 1))
+        return invalid("the state's slot stride must cover its rows");
+    if (!elem_aligned(a->x, eb) || !elem_aligned(a->y, eb) || (stateful && !elem_aligned(a->state, eb)) ||
+        !elem_aligned(a->cu_seqlens, 4))
+        return misaligned("a pointer is not aligned to its element size");
+    if (a->nseq == 0) return MS_OK;   // nothing to read or write
+    int sms = 0;
+    st = device_sms(&sms);
+    if (st != MS_OK) return st;
+    ms::ConvPackedParams p{};
+    p.tokens = a->tokens; p.channels = a->channels; p.nseq = a->nseq;
+    p.slots = a->state || a->state_indices ? a->slots : a->nseq;
+    p.x = a->x; p.x_st = a->x_token_stride;
+    p.y = a->y; p.y_st = a->y_token_stride;
+    if (stateful) { p.state = a->state; p.st_slot = a->state_slot_stride; p.st_row = a->state_row_stride; }
+    p.cu = a->cu_seqlens; p.idx = a->state_indices; p.has_init = a->has_initial_state;
+    p.weight = c->weight; p.bias = c->bias; p.width = c->width; p.silu = c->silu;
+    const cudaError_t e = ms::launch_conv_packed(p, a->in_dtype, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MS_OK : cuda_fail(e, "packed convolution launch");
+}
+
+ms_status mamba_ssd_state_update(const ms_ssd_update_args *a, void *stream) {
+    const CallRange range("mamba_ssd_state_update");
+    if (!a) return invalid("args is NULL");
+    const int eb = dtype_bytes(a->in_dtype);
+    if (!eb) return invalid("in_dtype");
+    if (a->batch < 0 || a->nheads <= 0 || a->ngroups <= 0 || a->headdim <= 0 || a->dstate <= 0)
+        return invalid("batch must not be negative, nheads, ngroups, headdim and dstate must be positive");
+    if (a->nheads % a->ngroups != 0) return invalid("nheads must be a multiple of ngroups");
+    if (a->dstate > MS_SSD_UPDATE_MAX_DSTATE) return unsupported("dstate above 256");
+    if (a->batch > 65535) return unsupported("batch above 65535");
+    if (a->nheads > 65535 || a->headdim > 65535 || a->nheads * a->headdim > (int64_t(1) << 30))
+        return unsupported("nheads or headdim above 65535, or their product above 2^30");
+    ms_status st = check_slots(a->batch, a->slots, a->state, a->state_indices, nullptr, true);
+    if (st != MS_OK) return st;
+    if (a->batch == 0) return MS_OK;
+    if (!a->state || !a->x || !a->dt || !a->B || !a->C || !a->y || !a->A)
+        return invalid("state, x, dt, B, C, y and A are required");
+    const int64_t per = a->nheads * a->headdim;
+    if (a->x_batch_stride < 0 || a->dt_batch_stride < 0 || a->B_batch_stride < 0 || a->C_batch_stride < 0 ||
+        (a->z && a->z_batch_stride < 0))
+        return invalid("strides must be non-negative");
+    if ((a->batch > 1 && a->y_batch_stride < per) || (a->slots > 1 && a->state_slot_stride < per * a->dstate))
+        return invalid("the strides of y and of the state's slots must cover their entries");
+    if (!elem_aligned(a->x, eb) || !elem_aligned(a->dt, eb) || !elem_aligned(a->B, eb) || !elem_aligned(a->C, eb) ||
+        (a->z && !elem_aligned(a->z, eb)) || !elem_aligned(a->y, eb) || !elem_aligned(a->state, 4) ||
+        !elem_aligned(a->A, 4) || (a->D && !elem_aligned(a->D, 4)) || (a->dt_bias && !elem_aligned(a->dt_bias, 4)))
+        return misaligned("a pointer is not aligned to its element size");
+    ms::SsdUpdateParams p{};
+    p.batch = a->batch; p.slots = a->slots;
+    p.nheads = static_cast<int>(a->nheads); p.hpg = static_cast<int>(a->nheads / a->ngroups);
+    p.headdim = static_cast<int>(a->headdim); p.dstate = static_cast<int>(a->dstate);
+    p.state = a->state; p.s_slot = a->state_slot_stride;
+    p.x = a->x; p.x_sb = a->x_batch_stride;
+    p.dt = a->dt; p.dt_sb = a->dt_batch_stride;
+    p.B = a->B; p.B_sb = a->B_batch_stride;
+    p.C = a->C; p.C_sb = a->C_batch_stride;
+    p.z = a->z; p.z_sb = a->z_batch_stride;
+    p.y = a->y; p.y_sb = a->y_batch_stride;
+    p.A = a->A; p.D = a->D; p.dt_bias = a->dt_bias;
+    p.idx = a->state_indices;
+    p.softplus = a->dt_softplus ? 1 : 0;
+    const cudaError_t e = ms::launch_ssd_update(p, a->in_dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MS_OK : cuda_fail(e, "SSD state update launch");
+}
+
+// What the forward and the backward norm share.
+static ms_status check_norm(const ms_norm_args *a) {
+    if (!a) return invalid("args is NULL");
+    if (!dtype_bytes(a->in_dtype)) return invalid("in_dtype");
+    if (a->reserved != 0) return invalid("reserved must be 0");
+    if (a->rows < 0 || a->dim <= 0 || a->group_size <= 0) return invalid("rows, dim or group_size out of range");
+    if (a->dim % a->group_size != 0) return invalid("dim must be a multiple of group_size");
+    if (a->dim > (int64_t(1) << 30) || a->rows > kMaxRows || a->rows * (a->dim / a->group_size) > kMaxRows)
+        return unsupported("dim above 2^30 or rows times groups above 2^31 - 1");
+    if (!(a->eps >= 0.f) || a->eps > 3e38f) return invalid("eps must be finite and not negative");
+    if (a->gate_first != 0 && a->gate_first != 1) return invalid("gate_first must be 0 or 1");
+    if ((a->residual || a->residual_out) &&
+        (!dtype_bytes(a->residual_dtype) || (a->in_dtype == MS_F32 && a->residual_dtype != MS_F32)))
+        return invalid("residual_dtype must be in_dtype or MS_F32");
+    if (a->x_row_stride < 0 || (a->z && a->z_row_stride < 0) || (a->residual && a->residual_row_stride < 0))
+        return invalid("strides must be non-negative");
+    const int eb = dtype_bytes(a->in_dtype), rb = dtype_bytes(a->residual_dtype);
+    if ((a->x && !elem_aligned(a->x, eb)) || (a->z && !elem_aligned(a->z, eb)) ||
+        (a->residual && !elem_aligned(a->residual, rb)) || (a->residual_out && !elem_aligned(a->residual_out, rb)) ||
+        (a->weight && !elem_aligned(a->weight, 4)))
+        return misaligned("a pointer is not aligned to its element size");
+    return MS_OK;
+}
+
+static ms::NormParams norm_params(const ms_norm_args *a) {
+    ms::NormParams p{};
+    p.rows = a->rows; p.dim = a->dim; p.gs = a->group_size; p.groups = a->dim / a->group_size;
+    p.x = a->x; p.x_sr = a->x_row_stride;
+    p.z = a->z; p.z_sr = a->z_row_stride;
+    p.res = a->residual; p.res_sr = a->residual_row_stride;
+    p.ro = a->residual_out; p.ro_sr = a->residual_out_row_stride;
+    p.y = a->y; p.y_sr = a->y_row_stride;
+    p.w = a->weight;
+    p.eps = a->eps; p.scale = a->residual_scale;
+    p.inv_gs = 1.f / static_cast<float>(a->group_size);
+    p.gate_first = a->gate_first;
+    return p;
+}
+
+ms_status mamba_norm_fwd(const ms_norm_args *a, void *stream) {
+    const CallRange range("mamba_norm_fwd");
+    ms_status st = check_norm(a);
+    if (st != MS_OK) return st;
+    if (a->rows == 0) return MS_OK;
+    if (!a->x || !a->y) return invalid("x and y are required");
+    if ((a->residual != nullptr) != (a->residual_out != nullptr))
+        return invalid("residual and residual_out are given together");
+    if (a->rows > 1 && (a->y_row_stride < a->dim || (a->residual_out && a->residual_out_row_stride < a->dim)))
+        return invalid("the row strides of y and residual_out must cover dim elements");
+    if (!elem_aligned(a->y, dtype_bytes(a->in_dtype))) return misaligned("a pointer is not aligned to its element size");
+    const cudaError_t e = ms::launch_norm_fwd(norm_params(a), a->in_dtype,
+                                              a->residual ? a->residual_dtype : a->in_dtype,
+                                              static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MS_OK : cuda_fail(e, "norm launch");
+}
+
+static ms_status norm_slabs(const ms_norm_args *a, int64_t *slabs) {
+    int sms = 0;
+    const ms_status st = device_sms(&sms);
+    if (st != MS_OK) return st;
+    *slabs = ms::norm_bwd_slabs(a->rows, a->dim, a->group_size, sms);
+    return MS_OK;
+}
+
+ms_status mamba_norm_bwd_workspace_size(const ms_norm_args *a, size_t *bytes) {
+    if (!bytes) return invalid("bytes is NULL");
+    *bytes = 0;
+    ms_status st = check_norm(a);
+    if (st != MS_OK) return st;
+    if (a->rows == 0) return MS_OK;
+    int64_t slabs = 0;
+    st = norm_slabs(a, &slabs);
+    if (st != MS_OK) return st;
+    *bytes = slabs > 1 ? static_cast<size_t>(slabs) * static_cast<size_t>(a->dim) * sizeof(float) : 0;
+    return MS_OK;
+}
+
+ms_status mamba_norm_bwd(const ms_norm_args *a, const ms_norm_bwd_args *g, void *workspace, size_t workspace_bytes,
+                         void *stream) {
+    const CallRange range("mamba_norm_bwd");
+    ms_status st = check_norm(a);
+    if (st != MS_OK) return st;
+    if (!g) return invalid("bwd is NULL");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (g->dweight && !elem_aligned(g->dweight, 4)) return misaligned("dweight is not aligned to 4 bytes");
+    if (a->rows == 0) {
+        if (!g->dweight) return MS_OK;
+        const cudaError_t e = cudaMemsetAsync(g->dweight, 0, static_cast<size_t>(a->dim) * sizeof(float), s);
+        return e == cudaSuccess ? MS_OK : cuda_fail(e, "clearing dweight");
+    }
+    const bool res = a->residual_out != nullptr;
+    const int eb = dtype_bytes(a->in_dtype), rb = res ? dtype_bytes(a->residual_dtype) : 4;
+    const bool need_x = !res || (a->z && a->gate_first);
+    if (!g->dy || !g->dx || (need_x && !a->x) || (a->z && !g->dz) || (res && !g->dresidual))
+        return invalid("dy and dx are required, x, dz with z and dresidual with a residual too");
+    if (!res && (g->dresidual || g->dresidual_out)) return invalid("residual gradients need residual_out");
+    if (g->dy_row_stride < 0 || (g->dresidual_out && g->dresidual_out_row_stride < 0) ||
+        (res && a->residual_out_row_stride < 0))
+        return invalid("strides must be non-negative");
+    if (a->rows > 1 && (g->dx_row_stride < a->dim || (a->z && g->dz_row_stride < a->dim) ||
+                        (res && g->dresidual_row_stride < a->dim)))
+        return invalid("the row strides of dx, dz and dresidual must cover dim elements");
+    if (!elem_aligned(g->dy, eb) || !elem_aligned(g->dx, eb) || (a->z && !elem_aligned(g->dz, eb)) ||
+        (res && !elem_aligned(g->dresidual, rb)) || (g->dresidual_out && !elem_aligned(g->dresidual_out, rb)))
+        return misaligned("a gradient pointer is not aligned to its element size");
+    int64_t slabs = 0;
+    st = norm_slabs(a, &slabs);
+    if (st != MS_OK) return st;
+    ms::NormBwdParams q{};
+    q.dy = g->dy; q.dy_sr = g->dy_row_stride;
+    q.dro = g->dresidual_out; q.dro_sr = g->dresidual_out_row_stride;
+    q.dx = g->dx; q.dx_sr = g->dx_row_stride;
+    q.dz = a->z ? g->dz : nullptr; q.dz_sr = g->dz_row_stride;
+    q.dres = g->dresidual; q.dres_sr = g->dresidual_row_stride;
+    q.dw = g->dweight;
+    q.slabs = slabs;
+    q.need_x = need_x;
+    if (g->dweight) {
+        if (slabs == 1) {
+            q.partial = g->dweight;
+        } else {
+            const size_t need = static_cast<size_t>(slabs) * static_cast<size_t>(a->dim) * sizeof(float);
+            if (!workspace || workspace_bytes < need) {
+                set_error("workspace of %zu bytes needed, %zu given", need,
+                          workspace ? workspace_bytes : static_cast<size_t>(0));
+                return MS_ERR_WORKSPACE;
+            }
+            if (!elem_aligned(workspace, 16)) return misaligned("workspace must be 16-byte aligned");
+            q.partial = static_cast<float *>(workspace);
+        }
+    }
+    const cudaError_t e = ms::launch_norm_bwd(norm_params(a), q, a->in_dtype, res ? a->residual_dtype : a->in_dtype, s);
+    return e == cudaSuccess ? MS_OK : cuda_fail(e, "norm backward launch");
+}
+
 }  // extern "C"

@@ -196,6 +196,74 @@ size_t ssd_persistent_ws_bytes(int ctas);
 size_t ssd_flag_offset();
 size_t ssd_carry_offset(int ctas);
 
+// ---- Mamba-2 serving operators (packed sequences, states in slots) ----------
+// cu: nseq + 1 row offsets or null (single tokens); idx: slot of each sequence
+// or null (its own number); has_init: bytes or null.
+
+// Causal depthwise convolution (conv_packed.cu). state: (slots, width - 1,
+// channels) of the input type or null, element strides st_slot and st_row.
+struct ConvPackedParams {
+    int64_t tokens, channels, nseq, slots;
+    const void *x;     int64_t x_st;
+    void *y;           int64_t y_st;
+    void *state;       int64_t st_slot, st_row;
+    const int32_t *cu, *idx;
+    const uint8_t *has_init;
+    const float *weight, *bias;
+    int width, silu;
+    int64_t tile;             // rows per tile block (set by the launch)
+};
+cudaError_t launch_conv_packed(const ConvPackedParams &p, int in_dtype, int num_sms, cudaStream_t stream);
+
+// Mamba-2 state update (ssd_update.cu). Strides in elements; the inner axes are contiguous.
+struct SsdUpdateParams {
+    int64_t batch, slots;
+    int nheads, hpg, headdim, dstate;   // hpg: heads per group
+    float *state;      int64_t s_slot;
+    const void *x;     int64_t x_sb;
+    const void *dt;    int64_t dt_sb;
+    const void *B;     int64_t B_sb;
+    const void *C;     int64_t C_sb;
+    const void *z;     int64_t z_sb;
+    void *y;           int64_t y_sb;
+    const float *A, *D, *dt_bias;
+    const int32_t *idx;
+    int softplus;
+    int row_blocks;           // blocks per head (set by the launch)
+};
+cudaError_t launch_ssd_update(const SsdUpdateParams &p, int in_dtype, cudaStream_t stream);
+
+// RMS norm (norm.cu). res / ro: residual and the sum residual_out, of type
+// res_dtype; in the backward only ro is read. w: weight or null.
+struct NormParams {
+    int64_t rows, dim, gs, groups;
+    const void *x;     int64_t x_sr;
+    const void *z;     int64_t z_sr;
+    const void *res;   int64_t res_sr;
+    void *ro;          int64_t ro_sr;
+    void *y;           int64_t y_sr;
+    const float *w;
+    float eps, scale, inv_gs;
+    int gate_first;
+    int team;                 // threads per (row, group) (set by the launch)
+};
+struct NormBwdParams {
+    const void *dy;    int64_t dy_sr;
+    const void *dro;   int64_t dro_sr;
+    void *dx;          int64_t dx_sr;
+    void *dz;          int64_t dz_sr;
+    void *dres;        int64_t dres_sr;
+    float *dw;
+    float *partial;           // (slabs, dim) shares of dw; dw itself for one slab; null without dw
+    int64_t slabs;            // row slabs per group
+    int need_x;               // x is read (the branch enters the norm by itself, or has a gate)
+};
+// Slabs the backward takes for these sizes.
+int64_t norm_bwd_slabs(int64_t rows, int64_t dim, int64_t gs, int num_sms);
+cudaError_t launch_norm_fwd(const NormParams &p, int in_dtype, int res_dtype, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const NormParams &p, const NormBwdParams &g, int in_dtype, int res_dtype,
+                            cudaStream_t stream);
+
 // Record the message that mamba_last_error() returns on this thread.
 void record_error(const char *fmt, ...);
 

@@ -1,0 +1,98 @@
+// Vectors of 1 to 8 consecutive elements in one memory access, and the checks
+// that choose their width.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "device_math.cuh"
+
+namespace ms {
+
+struct alignas(16) Raw32 { uint4 a, b; };   // eight float32 beside eight bfloat16
+
+template <int BYTES> struct RawOf;
+template <> struct RawOf<32> { using type = Raw32; };
+template <> struct RawOf<16> { using type = uint4; };
+template <> struct RawOf<8> { using type = uint2; };
+template <> struct RawOf<4> { using type = uint32_t; };
+template <> struct RawOf<2> { using type = uint16_t; };
+
+template <typename T, int VEC> using Raw = typename RawOf<VEC * (int)sizeof(T)>::type;
+
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> load_raw(const T *p) {
+    if constexpr (sizeof(T) * VEC == 32)
+        return {__ldg(reinterpret_cast<const uint4 *>(p)), __ldg(reinterpret_cast<const uint4 *>(p) + 1)};
+    else
+        return __ldg(reinterpret_cast<const Raw<T, VEC> *>(p));
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_raw(T *p, const Raw<T, VEC> &r) {
+    *reinterpret_cast<Raw<T, VEC> *>(p) = r;
+}
+
+// Widen one raw vector to float32 (exact).
+template <typename T, int VEC>
+__device__ __forceinline__ void widen(const Raw<T, VEC> &r, float (&v)[VEC]) {
+    union { Raw<T, VEC> r; T t[VEC]; uint32_t w[(VEC * sizeof(T) + 3) / 4]; } u;
+    u.r = r;
+    if constexpr (sizeof(T) == 2 && VEC >= 2) {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            v[2 * i] = bf16_lo(u.w[i]);
+            v[2 * i + 1] = bf16_hi(u.w[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = to_f32<T>(u.t[i]);
+    }
+}
+
+// Round to the storage type (bf16: to nearest even).
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> narrow(const float (&v)[VEC]) {
+    union { Raw<T, VEC> r; T t[VEC]; __nv_bfloat162 b[(VEC + 1) / 2]; } u;
+    if constexpr (sizeof(T) == 2 && VEC >= 2) {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) u.b[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) u.t[i] = from_f32<T>(v[i]);
+    }
+    return u.r;
+}
+
+// VEC float32 values from a pointer aligned to min(16, 4 VEC) bytes.
+template <int VEC>
+__device__ __forceinline__ void load_f32(const float *p, float (&v)[VEC]) {
+    if constexpr (VEC >= 4) {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            const float4 q = __ldg(reinterpret_cast<const float4 *>(p) + i);
+            v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+        }
+    } else if constexpr (VEC == 2) {
+        const float2 q = __ldg(reinterpret_cast<const float2 *>(p));
+        v[0] = q.x; v[1] = q.y;
+    } else {
+        v[0] = __ldg(p);
+    }
+}
+
+// Whether a tensor (NULL: always) with this row stride, in elements of eb
+// bytes, can be accessed in vectors of vec elements that start at multiples of vec.
+inline bool vec_ok(const void *ptr, int64_t stride, int eb, int vec) {
+    const int64_t bytes = static_cast<int64_t>(vec) * eb < 16 ? static_cast<int64_t>(vec) * eb : 16;
+    return !ptr || (reinterpret_cast<uintptr_t>(ptr) % bytes == 0 && (stride * eb) % bytes == 0);
+}
+
+// sigmoid(z) = 1 / (1 + e^-z); e^-z = inf gives 0.
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+// softplus to float32 rounding, for values computed once per (token, head).
+__device__ __forceinline__ float softplus_precise(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+
+}  // namespace ms
