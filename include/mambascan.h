@@ -645,6 +645,51 @@ typedef struct ms_conv_packed_args {
 ms_status mamba_conv_packed_fwd(const ms_conv_packed_args *args, const ms_conv1d_args *conv, void *stream);
 
 /*
+ * Mamba-2 scalar-decay SSM over packed sequences (the recurrence of
+ * mamba_ssd_fwd, headdim 64, dstate 128, bf16 inputs):
+ *   x, z, y : (tokens, nheads, 64), dt : (tokens, nheads),
+ *   B, C    : (tokens, ngroups, 128); token strides given, inner axes contiguous
+ *   state   : (slots, nheads, 64, 128) float32, updated in place; slot stride
+ *             given (a multiple of 4), inner axes contiguous, 16-byte aligned
+ * Alignment as in mamba_ssd_fwd. max_seqlen: the longest sequence as far as the
+ * host knows it (0: not known); it steers the schedule only.
+ */
+typedef struct ms_ssd_packed_args {
+    int64_t tokens, nseq, nheads, ngroups, slots, max_seqlen;
+    int32_t in_dtype;        /* MS_BF16 */
+    int32_t dt_softplus;
+    const void *x;      int64_t x_token_stride;
+    const void *dt;     int64_t dt_token_stride;
+    const void *B;      int64_t B_token_stride;
+    const void *C;      int64_t C_token_stride;
+    const void *z;      int64_t z_token_stride;    /* z may be NULL */
+    void *y;            int64_t y_token_stride;
+    const float *A;
+    const float *D;
+    const float *dt_bias;
+    float *state;       int64_t state_slot_stride;
+    const int32_t *cu_seqlens;
+    const int32_t *state_indices;
+    const uint8_t *has_initial_state;
+    uint32_t wait_limit_us;  /* limit of each internal wait in microseconds, 0 = about one second */
+    int32_t reserved;        /* 0 */
+} ms_ssd_packed_args;
+
+/* Workspace of mamba_ssd_packed_fwd for these arguments on the current device:
+ * a status word and, when long sequences are cut into segments that run side
+ * by side, the state each segment adds. */
+ms_status mamba_ssd_packed_workspace_size(const ms_ssd_packed_args *args, size_t *bytes);
+
+/*
+ * One or two kernel launches on `stream`. The workspace (256-byte aligned, of
+ * at least mamba_ssd_packed_workspace_size bytes) starts with a status word
+ * with mamba_ssd_fwd's meaning: 0 after a normal run, MS_ERR_TIMEOUT when an
+ * internal wait gave up (outputs and states are then incomplete).
+ */
+ms_status mamba_ssd_packed_fwd(const ms_ssd_packed_args *args, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
  * One token per request through the Mamba-2 recurrence, states in slots:
  *   x, z, y : (batch, nheads, headdim), dt : (batch, nheads),
  *   B, C    : (batch, ngroups, dstate); batch strides given, inner axes contiguous

@@ -27,6 +27,7 @@ __all__ = [
     "Conv1dArgs", "conv_scan_fwd", "conv_state_update", "build_conv_args", "trap_scan_fwd",
     "ScanBwdArgs", "scan_bwd", "SsdArgs", "build_ssd_args", "ssd_fwd", "ssd_check", "SSD_WORKSPACE_BYTES",
     "ConvPackedArgs", "conv_packed_fwd", "conv_packed_update", "SsdUpdateArgs", "ssd_state_update",
+    "SsdPackedArgs", "ssd_packed_fwd",
     "NormArgs", "NormBwdArgs", "norm_fwd", "norm_bwd",
     "MAX_DSTATE", "probe_unit_throughput", "PROBE_UNITS", "plan_workspace_size", "scan_status",
 ]
@@ -136,6 +137,24 @@ class SsdUpdateArgs(ctypes.Structure):
         ("z", _vp), ("z_batch_stride", _i64),
         ("y", _vp), ("y_batch_stride", _i64),
         ("A", _vp), ("D", _vp), ("dt_bias", _vp), ("state_indices", _vp),
+    ]
+
+
+class SsdPackedArgs(ctypes.Structure):
+    """Mirror of ``ms_ssd_packed_args``."""
+    _fields_ = [
+        ("tokens", _i64), ("nseq", _i64), ("nheads", _i64), ("ngroups", _i64), ("slots", _i64), ("max_seqlen", _i64),
+        ("in_dtype", _i32), ("dt_softplus", _i32),
+        ("x", _vp), ("x_token_stride", _i64),
+        ("dt", _vp), ("dt_token_stride", _i64),
+        ("B", _vp), ("B_token_stride", _i64),
+        ("C", _vp), ("C_token_stride", _i64),
+        ("z", _vp), ("z_token_stride", _i64),
+        ("y", _vp), ("y_token_stride", _i64),
+        ("A", _vp), ("D", _vp), ("dt_bias", _vp),
+        ("state", _vp), ("state_slot_stride", _i64),
+        ("cu_seqlens", _vp), ("state_indices", _vp), ("has_initial_state", _vp),
+        ("wait_limit_us", ctypes.c_uint32), ("reserved", _i32),
     ]
 
 
@@ -260,6 +279,11 @@ def load_library():
         lib.mamba_conv_packed_fwd.argtypes = [ctypes.POINTER(ConvPackedArgs), ctypes.POINTER(Conv1dArgs), _vp]
         lib.mamba_ssd_state_update.restype = ctypes.c_int
         lib.mamba_ssd_state_update.argtypes = [ctypes.POINTER(SsdUpdateArgs), _vp]
+        lib.mamba_ssd_packed_workspace_size.restype = ctypes.c_int
+        lib.mamba_ssd_packed_workspace_size.argtypes = [ctypes.POINTER(SsdPackedArgs),
+                                                        ctypes.POINTER(ctypes.c_size_t)]
+        lib.mamba_ssd_packed_fwd.restype = ctypes.c_int
+        lib.mamba_ssd_packed_fwd.argtypes = [ctypes.POINTER(SsdPackedArgs), _vp, ctypes.c_size_t, _vp]
         lib.mamba_norm_fwd.restype = ctypes.c_int
         lib.mamba_norm_fwd.argtypes = [ctypes.POINTER(NormArgs), _vp]
         lib.mamba_norm_bwd_workspace_size.restype = ctypes.c_int
@@ -884,6 +908,69 @@ def conv_packed_update(state, x, weight, bias=None, silu=True, state_indices=Non
     continuing from slot ``state_indices[b]`` (None: slot b) of ``state``,
     which takes the token in place. Skipped rows as :func:`conv_packed_fwd`."""
     return _conv_packed(x, weight, bias, silu, None, x.shape[0], state, state_indices, None, out, stream)
+
+
+def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_softplus=True, state=None,
+                   state_indices=None, has_initial_state=None, max_seqlen=0, out=None, workspace=None, check=True,
+                   stream=None, wait_limit_us=0):
+    """Mamba-2 scalar-decay SSM over packed sequences (chunked SSD on the tensor cores).
+
+    The recurrence of :func:`ssd_fwd` for sequences packed one behind the
+    other: x, z (tokens, nheads, 64), dt (tokens, nheads), B, C (tokens,
+    ngroups, 128) bfloat16, the axes behind the tokens contiguous (slices of a
+    wider row are fine); A, D, dt_bias (nheads,) float32. ``cu_seqlens``,
+    ``state_indices`` and ``has_initial_state`` as :func:`conv_packed_fwd`;
+    ``state`` (slots, nheads, 64, 128) float32 is updated in place (None:
+    every sequence starts from zero and leaves no state). ``max_seqlen``: the
+    longest sequence if the host knows it; it steers the schedule only.
+    Returns y (tokens, nheads, 64); rows of no or of a skipped sequence are not
+    written. ``workspace``: a uint8 CUDA tensor, allocated here when None or too
+    small. With ``check`` the call synchronizes the stream and raises if the
+    kernel reported a failed wait; without it, pass a workspace and call
+    :func:`ssd_check` on it later.
+    """
+    torch = _torch()
+    _need_cuda("x", x, None, 3)
+    tokens, nheads = x.shape[0], x.shape[1]
+    nseq = _need_cu_seqlens(cu_seqlens)
+    y = torch.empty((tokens, nheads, SSD_HEADDIM), dtype=x.dtype, device=x.device) if out is None else out
+    _need_cuda("B", B, x.dtype, 3)
+    ngroups = B.shape[1]
+    for name, t, shape in (("x", x, (tokens, nheads, SSD_HEADDIM)), ("out", y, (tokens, nheads, SSD_HEADDIM)),
+                           ("z", z, (tokens, nheads, SSD_HEADDIM)), ("dt", dt, (tokens, nheads)),
+                           ("B", B, (tokens, ngroups, SSD_DSTATE)), ("C", C, (tokens, ngroups, SSD_DSTATE))):
+        _need_rows(name, t, x.dtype, shape)
+    for name, t in (("A", A), ("D", D), ("dt_bias", dt_bias)):
+        _need_heads(name, t, nheads)
+    _need_slots(nseq, state, state_indices, has_initial_state)
+    a = SsdPackedArgs()
+    if state is not None:
+        _need_cuda("state", state, torch.float32, 4)
+        if tuple(state.shape[1:]) != (nheads, SSD_HEADDIM, SSD_DSTATE) or not state[:1].is_contiguous():
+            raise ValueError(f"state must be (slots, {nheads}, 64, 128) float32, contiguous behind the slots")
+        a.slots, a.state, a.state_slot_stride = state.shape[0], _ptr(state), state.stride(0)
+    _same_device(x.device, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, cu_seqlens=cu_seqlens, state=state,
+                 state_indices=state_indices, has_initial_state=has_initial_state, out=y, workspace=workspace)
+    a.tokens, a.nseq, a.nheads, a.ngroups, a.max_seqlen = tokens, nseq, nheads, ngroups, int(max_seqlen)
+    a.in_dtype, a.dt_softplus = _dtype_code(x), 1 if dt_softplus else 0
+    for name, t in (("x", x), ("dt", dt), ("B", B), ("C", C), ("z", z), ("y", y)):
+        if t is not None:
+            setattr(a, name, _ptr(t))
+            setattr(a, f"{name}_token_stride", t.stride(0) if tokens > 1 else t.shape[1:].numel())
+    a.A, a.D, a.dt_bias = _ptr(A), _ptr(D), _ptr(dt_bias)
+    a.cu_seqlens, a.state_indices, a.has_initial_state = _ptr(cu_seqlens), _ptr(state_indices), _ptr(has_initial_state)
+    a.wait_limit_us = int(wait_limit_us)
+    lib = load_library()
+    n = _workspace_bytes(x.device, lib.mamba_ssd_packed_workspace_size, a)
+    own_ws = workspace is None or workspace.numel() < n
+    if own_ws:
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _call(x.device, lib.mamba_ssd_packed_fwd, ctypes.byref(a), workspace.data_ptr(), workspace.numel(), stream=stream)
+    if own_ws:
+        _keep_until_done(workspace, stream)
+    if check:
+        ssd_check(workspace, stream)
+    return y
 
 
 def ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, state_indices=None,

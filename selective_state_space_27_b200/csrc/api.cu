@@ -837,6 +837,109 @@ ms_status mamba_ssd_state_update(const ms_ssd_update_args *a, void *stream) {
     return e == cudaSuccess ? MS_OK : cuda_fail(e, "SSD state update launch");
 }
 
+static ms_status check_ssd_packed(const ms_ssd_packed_args *a) {
+    if (!a) return invalid("args is NULL");
+    if (a->nheads <= 0 || a->ngroups <= 0) return invalid("nheads and ngroups must be positive");
+    if (a->nheads % a->ngroups != 0) return invalid("nheads must be a multiple of ngroups");
+    if (a->reserved != 0) return invalid("reserved must be 0");
+    if (a->in_dtype != MS_BF16) {
+        if (a->in_dtype != MS_F32) return invalid("unknown in_dtype");
+        return unsupported("the SSD kernel takes bf16 inputs only");
+    }
+    if (a->tokens < 0 || a->tokens > kMaxRows - 64 * 1024 || a->max_seqlen < 0)
+        return invalid("tokens must be in [0, 2^31 - 2^16) and max_seqlen not negative");
+    if (a->nheads > 65535) return unsupported("nheads above 65535");
+    if (a->nseq < 0 || a->nseq * a->nheads > (int64_t(1) << 29) || a->nseq > (int64_t(1) << 29) ||
+        (a->tokens / 512 + a->nseq) * a->nheads > kMaxRows)
+        return unsupported("too many sequences or segments times heads for one launch");
+    const ms_status st = check_slots(a->nseq, a->slots, a->state, a->state_indices, a->has_initial_state, true);
+    if (st != MS_OK) return st;
+    if (a->nseq == 0) return MS_OK;
+    if (!a->cu_seqlens || !a->A) return invalid("cu_seqlens and A are required");
+    if (a->tokens > 0 && (!a->x || !a->dt || !a->B || !a->C || !a->y)) return invalid("x, dt, B, C and y are required");
+    if (a->tokens > 0) {
+        const int64_t xi = a->nheads * MS_SSD_HEADDIM, bi = a->ngroups * MS_SSD_DSTATE;
+        if (a->x_token_stride < xi || a->y_token_stride < xi || (a->z && a->z_token_stride < xi))
+            return invalid("the token stride of x, y and z must cover nheads * 64 elements");
+        if (a->B_token_stride < bi || a->C_token_stride < bi)
+            return invalid("the token stride of B and C must cover ngroups * 128 elements");
+        if (a->dt_token_stride < a->nheads) return invalid("the token stride of dt must cover nheads elements");
+        if (a->x_token_stride % 8 || a->y_token_stride % 8 || a->B_token_stride % 8 || a->C_token_stride % 8 ||
+            (a->z && a->z_token_stride % 8))
+            return misaligned("token strides of x, y, B, C (and z) must be multiples of 8 elements");
+        if (a->x_token_stride >= (int64_t(1) << 38) || a->B_token_stride >= (int64_t(1) << 38) ||
+            a->C_token_stride >= (int64_t(1) << 38))
+            return unsupported("a token stride of 2^38 elements or more");
+    }
+    if (a->state && (a->state_slot_stride < 0 ||
+                     (a->slots > 1 && a->state_slot_stride < a->nheads * MS_SSD_HEADDIM * MS_SSD_DSTATE)))
+        return invalid("the state's slot stride must cover its heads");
+    if (!elem_aligned(a->x, 16) || !elem_aligned(a->B, 16) || !elem_aligned(a->C, 16) || !elem_aligned(a->y, 16) ||
+        (a->z && !elem_aligned(a->z, 16)) || !elem_aligned(a->dt, 2) || !elem_aligned(a->A, 4) ||
+        (a->D && !elem_aligned(a->D, 4)) || (a->dt_bias && !elem_aligned(a->dt_bias, 4)) ||
+        (a->state && !elem_aligned(a->state, 4)) || !elem_aligned(a->cu_seqlens, 4))
+        return misaligned("x, y, B, C and z must be 16-byte aligned, the other pointers aligned to their elements");
+    return MS_OK;
+}
+
+static ms_status ssd_packed_segment(const ms_ssd_packed_args *a, int *chunks) {
+    int sms = 0;
+    const ms_status st = device_sms(&sms);
+    if (st != MS_OK) return st;
+    *chunks = ms::ssd_packed_segment(a->tokens, a->nseq, a->nheads, a->max_seqlen, sms);
+    return MS_OK;
+}
+
+ms_status mamba_ssd_packed_workspace_size(const ms_ssd_packed_args *a, size_t *bytes) {
+    if (!bytes) return invalid("bytes is NULL");
+    *bytes = 0;
+    ms_status st = check_ssd_packed(a);
+    if (st != MS_OK) return st;
+    int chunks = 0;
+    st = ssd_packed_segment(a, &chunks);
+    if (st != MS_OK) return st;
+    *bytes = ms::ssd_packed_ws_bytes(a->tokens, a->nseq, a->nheads, chunks);
+    return MS_OK;
+}
+
+ms_status mamba_ssd_packed_fwd(const ms_ssd_packed_args *a, void *workspace, size_t workspace_bytes, void *stream) {
+    const CallRange range("mamba_ssd_packed_fwd");
+    ms_status st = check_ssd_packed(a);
+    if (st != MS_OK) return st;
+    int chunks = 0;
+    st = ssd_packed_segment(a, &chunks);
+    if (st != MS_OK) return st;
+    const size_t need = ms::ssd_packed_ws_bytes(a->tokens, a->nseq, a->nheads, chunks);
+    if (!workspace || workspace_bytes < need) {
+        set_error("workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : static_cast<size_t>(0));
+        return MS_ERR_WORKSPACE;
+    }
+    if (!elem_aligned(workspace, 256)) return misaligned("workspace must be 256-byte aligned");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a->nseq == 0) {
+        const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), s);
+        return e == cudaSuccess ? MS_OK : cuda_fail(e, "clearing the status word");
+    }
+    ms::SsdPackedParams p{};
+    p.tokens = a->tokens; p.nseq = a->nseq; p.nheads = a->nheads; p.ngroups = a->ngroups; p.slots = a->slots;
+    p.x = a->x; p.x_st = a->x_token_stride;
+    p.dt = a->dt; p.dt_st = a->dt_token_stride;
+    p.B = a->B; p.B_st = a->B_token_stride;
+    p.C = a->C; p.C_st = a->C_token_stride;
+    p.z = a->z; p.z_st = a->z_token_stride;
+    p.y = a->y; p.y_st = a->y_token_stride;
+    p.A = a->A; p.D = a->D; p.dt_bias = a->dt_bias;
+    p.state = a->state; p.s_slot = a->state_slot_stride;
+    p.cu = a->cu_seqlens; p.idx = a->state_indices; p.has_init = a->has_initial_state;
+    p.softplus = a->dt_softplus ? 1 : 0;
+    p.wait_limit_ns = a->wait_limit_us ? 1000ull * a->wait_limit_us : 1000000000ull;
+    p.seg_chunks = chunks;
+    ms::ssd_packed_bind(p, workspace);
+    const cudaError_t e = ms::launch_ssd_packed(p, s);
+    if (e == cudaErrorNotSupported) return unsupported("the driver offers no tensor-map encoder");
+    return e == cudaSuccess ? MS_OK : cuda_fail(e, "packed SSD launch");
+}
+
 // What the forward and the backward norm share.
 static ms_status check_norm(const ms_norm_args *a) {
     if (!a) return invalid("args is NULL");

@@ -264,6 +264,36 @@ cudaError_t launch_norm_fwd(const NormParams &p, int in_dtype, int res_dtype, cu
 cudaError_t launch_norm_bwd(const NormParams &p, const NormBwdParams &g, int in_dtype, int res_dtype,
                             cudaStream_t stream);
 
+// Mamba-2 SSD over packed sequences (ssd_packed.cu): bf16, headdim 64, dstate 128.
+struct SsdPackedParams {
+    int64_t tokens, nseq, nheads, ngroups, slots;
+    const void *x;     int64_t x_st;
+    const void *dt;    int64_t dt_st;
+    const void *B;     int64_t B_st;
+    const void *C;     int64_t C_st;
+    const void *z;     int64_t z_st;
+    void *y;           int64_t y_st;
+    const float *A, *D, *dt_bias;
+    float *state;      int64_t s_slot;
+    const int32_t *cu, *idx;
+    const uint8_t *has_init;
+    int softplus;
+    int *status;
+    uint64_t wait_limit_ns;
+    // Sequences are cut into segments of seg_chunks chunks of 128 tokens (0:
+    // not cut). seg_states: (segment places, nheads, 64, 128) zero-start end
+    // states, seg_decay: (segment places, nheads) their decays (log2).
+    int seg_chunks;
+    float *seg_states, *seg_decay;
+};
+// Chunks per segment for these sizes (0: sequences are not cut).
+int ssd_packed_segment(int64_t tokens, int64_t nseq, int64_t nheads, int64_t max_seqlen, int num_sms);
+// Places for segments: at least the number of segments of any split of tokens into nseq sequences.
+int64_t ssd_packed_places(int64_t tokens, int64_t nseq, int seg_chunks);
+size_t ssd_packed_ws_bytes(int64_t tokens, int64_t nseq, int64_t nheads, int seg_chunks);
+void ssd_packed_bind(SsdPackedParams &p, void *ws);
+cudaError_t launch_ssd_packed(const SsdPackedParams &p, cudaStream_t stream);
+
 // Record the message that mamba_last_error() returns on this thread.
 void record_error(const char *fmt, ...);
 
