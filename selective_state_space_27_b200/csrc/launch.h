@@ -280,6 +280,7 @@ struct SsdPackedParams {
     int softplus;
     int *status;
     uint64_t wait_limit_ns;
+    int y_wide;               // y rows allow 32-byte stores (set by the launch)
     // Sequences are cut into segments of seg_chunks chunks of 128 tokens (0:
     // not cut). seg_states: (segment places, nheads, 64, 128) zero-start end
     // states, seg_decay: (segment places, nheads) their decays (log2).

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kWarps * 32) ssd_update_vec_kernel(const SsdUp
     }
     float delta = to_f32<T>(__ldg(static_cast<const T *>(p.dt) + b * p.dt_sb + h));
     if (p.dt_bias) delta += __ldg(p.dt_bias + h);
-    if (p.softplus) delta = softplus_precise(delta);
+    if (p.softplus) delta = softplus_fine(delta);
     const float a = ex2_approx(delta * __ldg(p.A + h) * kLog2e);
     const float Dh = p.D ? __ldg(p.D + h) : 0.f;
     const T *xp = static_cast<const T *>(p.x) + b * p.x_sb + static_cast<int64_t>(h) * p.headdim;
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kWarps * 32) ssd_update_kernel(const SsdUpdate
     const T *Cp = static_cast<const T *>(p.C) + b * p.C_sb + static_cast<int64_t>(g) * p.dstate;
     float delta = to_f32<T>(__ldg(static_cast<const T *>(p.dt) + b * p.dt_sb + h));
     if (p.dt_bias) delta += __ldg(p.dt_bias + h);
-    if (p.softplus) delta = softplus_precise(delta);
+    if (p.softplus) delta = softplus_fine(delta);
     const float a = ex2_approx(delta * __ldg(p.A + h) * kLog2e);
     const int64_t at = static_cast<int64_t>(h) * p.headdim + row;
     const float x = to_f32<T>(__ldg(static_cast<const T *>(p.x) + b * p.x_sb + at));
