@@ -886,7 +886,7 @@ static ms_status ssd_packed_segment(const ms_ssd_packed_args *a, int *chunks) {
     int sms = 0;
     const ms_status st = device_sms(&sms);
     if (st != MS_OK) return st;
-    *chunks = ms::ssd_packed_segment(a->tokens, a->nseq, a->nheads, a->max_seqlen, sms);
+    *chunks = ms::ssd_packed_segment(a->tokens, a->nseq, a->nheads, a->ngroups, a->max_seqlen, sms);
     return MS_OK;
 }
 

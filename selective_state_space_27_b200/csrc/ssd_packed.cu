@@ -16,20 +16,24 @@
 // cancel. A token's decay is taken as at least 2^-160, which is 0 in float32
 // either way; it keeps the running sums small.
 //
-// Layout. One CTA walks one segment (see below) of one (sequence, head) with
-// two CTAs per SM, so that one's loads and tensor work overlap the other's
-// arithmetic: 100 KB of shared memory (X, B, C, the state's bf16 copy; the
-// split w X takes C's place, which is done with by then) and 256 columns of
-// tensor memory (G, overwritten in place by M' as the A operand of M' X; Y;
-// the state). The decayed state and the decayed inter-chunk term with the skip
-// are written into the accumulators, so the products add onto them.
-// Roles (320 threads): warps 0-7 arithmetic (warp w: rows 32 (w % 4) .. + 31
-// of the tile, column half w / 4, sixteen columns at a time: nothing may spill,
-// the L1 that shared memory leaves is far too small for it), warp 8 TMA loads
-// and step sizes, warp 9 tensor memory and MMA issue.
-// Order within a chunk: G and C H^T; w X and the start of Y; the state product
-// runs while the warps build M'; M' X runs while they pass the state on; B and C
-// of the next chunk are on their way since the state product ended.
+// Layout. On sm_100a an MMA of 128 rows takes 64 clocks for any N up to 128
+// (measured), so a product with N = 64, one head, wastes half of the tensor
+// core. One CTA per SM therefore walks one segment (see below) of TWO heads of
+// one group: they share B, C and G, and C H^T and B^T (w X) are products with
+// N = 128. Per chunk and pair of heads 48 MMAs, 3072 clocks, against 5120 one by
+// one. 512 columns of tensor memory: G; M' of both heads (the A operand of
+// M' X); Y and the states of both. 208 KB of shared memory: X twice (the next
+// chunk's loads while this one is worked on), B, C, the split w X and the
+// states' bf16 copies, whose place the lo term of w X takes between C H^T and
+// the next state. The decayed state and the decayed inter-chunk term with the
+// skip are written into the accumulators, so the products add onto them.
+// Roles (640 threads): warps 0-15 arithmetic (head w / 8; rows 32 (w % 4) ..
+// + 31 of the tile; columns by half, sixteen at a time: nothing may spill, the
+// L1 that shared memory leaves is too small for it), warps 16-17 the heads' step
+// sizes, warp 18 TMA loads, warp 19 tensor memory and MMA issue.
+// Order within a chunk: w X while G and C H^T run; the start of Y; M' while the
+// state product runs; the next state while M' X runs. Loads go out as soon as
+// their buffer was read for the last time.
 //
 // Long sequences with few heads are cut into segments that run side by side
 // (ssd_packed_segment): a first kernel computes what every segment but a
@@ -56,61 +60,93 @@ namespace {
 using namespace umma;
 
 constexpr int kQ = 128, kP = 64, kN = 128;
-constexpr int kWarpsC = 8;                        // arithmetic warps
-constexpr int kThreads = kWarpsC * 32 + 64;
-constexpr int kParts = kWarpsC / 4;               // column parts of an arithmetic warp group
-constexpr int kCQ = 4 / kParts;                   // column quarters (16 columns) per warp
-constexpr int kTmaWarp = kWarpsC, kMmaWarp = kWarpsC + 1;
+constexpr int kWarpsC = 16;                       // arithmetic warps, eight per head
+constexpr int kStepWarp = kWarpsC, kTmaWarp = kWarpsC + 2, kMmaWarp = kWarpsC + 3;
+constexpr int kThreads = (kWarpsC + 4) * 32;
 constexpr float kMinStep = -160.f;                // smallest log2 decay of one token
 
 // Shared memory from a 1024-byte aligned base; tiles of 128-byte-swizzled atoms.
 constexpr uint32_t kAtom = kQ * 128;              // 128 rows of 128 bytes
-constexpr uint32_t kOffX = 0;                     // X: 128 tokens x 64
-constexpr uint32_t kOffB = kAtom;                 // B: 128 tokens x 128, two atoms
-constexpr uint32_t kOffC = kOffB + 2 * kAtom;     // C, then the hi and lo terms of w X
-constexpr uint32_t kOffH = kOffC + 2 * kAtom;     // H (128 rows n x 64 bf16 along p)
-constexpr uint32_t kOffStep = kOffH + kAtom;      // two buffers of StepData
+constexpr uint32_t kOffX = 0;                     // X: two buffers x two heads x (128 tokens x 64)
+constexpr uint32_t kOffB = 4 * kAtom;             // B: 128 tokens x 128, two atoms
+constexpr uint32_t kOffC = 6 * kAtom;             // C (in the states kernel a second buffer of B)
+constexpr uint32_t kOffW = 8 * kAtom;             // the hi terms of w X of both heads
+constexpr uint32_t kOffH = 10 * kAtom;            // H of both heads (128 rows n x 64 bf16 along p each), or the lo terms
+constexpr uint32_t kOffStep = 12 * kAtom;         // StepData[kSteps][2 heads]
 struct StepData {
     float s[kQ];      // running sum of delta A (log2)
     float cf[kQ];     // 2^(s at the end of the token's 32-token block - s_i) delta_i
     float dl[kQ];     // delta_i
     float w[kQ];      // 2^(s_end - s_i) delta_i
 };
-constexpr uint32_t kOffBar = kOffStep + 2 * sizeof(StepData);
-// Barriers; chunk k completes phase k of each, step[k % 2] its phase k / 2:
+constexpr int kSteps = 4;                         // chunks of step data, made ahead of their use
+constexpr uint32_t kOffBar = kOffStep + kSteps * 2 * sizeof(StepData);
+// Barriers; chunk k completes phase k of each, xfull[k % 2] its phase k / 2 and
+// step[head][k % 4] its phase k / 4 (ystore, sfree alike). "Heads" are the live ones (the last pair of a
+// group with an odd number of heads has one):
 //   full    B and C of chunk k landed                        <- TMA bytes
 //   xfull   X of chunk k landed                              <- TMA bytes
-//   gfull   G(k) and C H^T(k) done: C is free                <- tcgen05.commit
-//   wready  w X and the start of Y of chunk k written        <- arithmetic warps
-//   mready  M' of chunk k written                            <- arithmetic warps
-//   sfull   the state after chunk k; B and w X are free, B and C of k + 1 go out  <- tcgen05.commit
-//   yfull   Y(k) done: X is free, X of k + 1 goes out        <- tcgen05.commit
-//   hready  state tile and accumulator for chunk k written, Y(k - 1) read  <- arithmetic warps
-//   step    step data of chunk k written                     <- 32 producer lanes
-// No waiter falls two phases behind: the next phase of full, xfull, gfull,
-// sfull and yfull needs wready(k + 1), which every arithmetic warp gives after
-// its waits for chunk k; the producer's loads follow its own waits for sfull(k)
-// and yfull(k), and sfull(k + 1) needs those loads; the issuer waits for
-// yfull(k) before G(k + 1); step data of chunk k + 2 follows yfull(k).
-enum Bar { kFull, kXFull, kGFull, kWReady, kMReady, kSFull, kYFull, kHReady, kStep0, kStep1, kDrain, kNumBars };
-constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;   // tensor memory address, abort flag, segment
-constexpr uint32_t kSmemBytes = kOffMisc + 32;
-static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+//   gfull   G(k) and C H^T(k) done: C and the state tile are free  <- tcgen05.commit
+//   wready  w X of chunk k written                           <- arithmetic warps of the heads
+//   mready  the start of Y and M' of chunk k written, G(k) read  <- arithmetic warps of the heads
+//   sfull   the states after chunk k; B, w X and the state tile are free  <- tcgen05.commit
+//   yfull   Y(k) done                                        <- tcgen05.commit
+//   ystore  y of chunk k in X's place, to be stored from there  <- arithmetic warps of the heads, of buffer k % 2
+//   sfree   the same: the step data of chunk k are free      <- tcgen05.commit, of buffer k % 4
+//   hready  state tile and accumulator for chunk k written   <- arithmetic warps of the heads
+//   yfree   Y(k) read                                        <- arithmetic warps of the heads
+//   step    step data of chunk k written                     <- 32 lanes of a step warp
+// No waiter falls two phases behind (a parity wait would then miss its phase):
+// the next phase of gfull, sfull and yfull needs wready or hready of chunk k + 1,
+// which every arithmetic warp gives after its waits for chunk k; that of full
+// needs the loading warp, behind its wait for sfull(k); those of ystore, sfree,
+// xfull and step of a buffer need that buffer filled again by the warp that waits
+// for it; and what the issuing warp waits for follows from what it issues later.
+enum Bar { kFull, kXFull0, kXFull1, kGFull, kWReady, kMReady, kSFull, kYFull, kYStore0, kYStore1,
+           kHReady, kYFree, kDrain, kStep0, kSFree0 = kStep0 + 2 * kSteps, kNumBars = kSFree0 + kSteps };
+constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;   // tensor memory address, abort flag
+constexpr uint32_t kSmemBytes = kOffMisc + 16;
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
-constexpr uint32_t kTmemCols = 256;
-constexpr uint32_t kColG = 0, kColY = 128, kColS = 192;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColG = 0, kColM = 128, kColY = 256, kColS = 384;   // M', Y and S: 64 columns per head
 
-// A bounded wait whose slow path is a call: the loop below waits in many places
-// and its code has to stay small for the instruction cache.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint64_t limit_ns)
+// Index of step data and its barrier's phase.
+__device__ __forceinline__ int step_of(int k) { return k & (kSteps - 1); }
+__device__ __forceinline__ uint32_t step_phase(int k) { return (uint32_t)(k / kSteps) & 1u; }
+
+// A bounded wait. When its limit runs out it records that in the status word and
+// raises the CTA's abort flag; from then on every wait of the CTA returns at once
+// and the roles run to their end on what is there: all addresses stay in bounds,
+// and the loads and MMAs in flight are still waited for before the CTA leaves.
+// The slow path is a call: the loops wait in many places and their code has to
+// stay small for the instruction cache.
+__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status,
+                                       uint64_t limit_ns)
 {
-    return role_wait(bar, parity, abort_flag, limit_ns);
+    const uint64_t t0 = global_ns();
+    while (!*abort_flag && !mbar_test(bar, parity))
+        if (global_ns() - t0 > limit_ns) give_up(status, abort_flag);
 }
 
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint64_t limit_ns)
-{
-    return mbar_test(bar, parity) || wait_slow(bar, parity, abort_flag, limit_ns);
-}
+struct Waiter {
+    uint32_t bars;
+    volatile int *abort_flag;
+    int *status;
+    uint64_t limit_ns;
+    // one thread
+    __device__ __forceinline__ void one(int b, uint32_t parity) const
+    {
+        const uint32_t at = bars + 8u * (uint32_t)b;
+        if (!mbar_test(at, parity)) wait_slow(at, parity, abort_flag, status, limit_ns);
+    }
+    // all lanes of a warp, together afterwards
+    __device__ __forceinline__ void operator()(int b, uint32_t parity) const
+    {
+        one(b, parity);
+        __syncwarp();
+    }
+};
 
 // What a CTA works on: chunks of 128 tokens from row `row`, `len` tokens, of
 // sequence `seq`; segment `seg` of `nseg`, whose first place is `base`.
@@ -209,23 +245,6 @@ __device__ __forceinline__ void token_sums(const float (&a)[4], int lane, float 
     }
 }
 
-// Split w x (eight values of row r, 16-byte piece q) into bf16 hi + lo and
-// store both into the operand tiles at `tile` (lo one atom further).
-__device__ __forceinline__ void store_split(uint32_t tile, int r, int q, const float2 (&x)[4], float w)
-{
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 a = mul2(x[e], f2(w, w));
-        hi[e] = pack_bf16(a.x, a.y);
-        const float2 d = add2(a, f2(-bf16_lo(hi[e]), -bf16_hi(hi[e])));
-        lo[e] = pack_bf16(d.x, d.y);
-    }
-    const uint32_t at = tile + sw128((uint32_t)r, (uint32_t)q);
-    st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-    st_shared_v4(at + kAtom, lo[0], lo[1], lo[2], lo[3]);
-}
-
 __device__ __forceinline__ void widen8(const uint4 &x, float2 (&v)[4])
 {
     v[0] = f2(bf16_lo(x.x), bf16_hi(x.x));
@@ -234,50 +253,54 @@ __device__ __forceinline__ void widen8(const uint4 &x, float2 (&v)[4])
     v[3] = f2(bf16_lo(x.w), bf16_hi(x.w));
 }
 
-// The state product B^T (w X), hi then lo, onto what the accumulator holds or in its place.
-__device__ __forceinline__ void issue_state_product(uint32_t tmem, uint32_t base, bool onto)
+// Split w x (eight values) into bf16 hi + lo.
+__device__ __forceinline__ void split(const uint4 &xr, float w, uint32_t (&hi)[4], uint32_t (&lo)[4])
 {
-    constexpr uint32_t id_s = bf16_idesc(128, 64, true, true);
-    const uint64_t b = sw128_desc(base + kOffB, kAtom, 1024), x = sw128_desc(base + kOffC, kAtom, 1024);
+    float2 x[4];
+    widen8(xr, x);
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            mma_bf16(tmem + kColS, b + (uint32_t)k * (2048u >> 4), x + (uint32_t)(t * kAtom + k * 2048u) / 16u, id_s,
-                     onto || t > 0 || k > 0);
-}
-
-// State values of this thread: n = 32 sub + lane, p = 16 cq .. + 15 for the column quarter cq; global
-// layout (p, n), so a warp's lanes are consecutive.
-__device__ __forceinline__ void load_state(const float *src, int r, int cq, float (&v)[16])
-{
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = src ? __ldcg(src + (16 * cq + j) * kN + r) : 0.f;
-}
-
-__device__ __forceinline__ void store_state(float *dst, int r, int cq, const float (&v)[16])
-{
-#pragma unroll
-    for (int j = 0; j < 16; ++j) __stcg(dst + (16 * cq + j) * kN + r, v[j]);
-}
-
-__device__ __forceinline__ void tmem_store16_scaled(uint32_t taddr, const float (&v)[16], float f)
-{
-    float a[16];
-#pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-        const float2 t = mul2(f2(v[j], v[j + 1]), f2(f, f));
-        a[j] = t.x;
-        a[j + 1] = t.y;
+    for (int e = 0; e < 4; ++e) {
+        const float2 a = mul2(x[e], f2(w, w));
+        hi[e] = pack_bf16(a.x, a.y);
+        const float2 d = add2(a, f2(-bf16_lo(hi[e]), -bf16_hi(hi[e])));
+        lo[e] = pack_bf16(d.x, d.y);
     }
-    tmem_store16(taddr, a);
 }
 
-__device__ __forceinline__ void state_tile(uint32_t tile, int r, int cq, const float (&v)[16])
+// The state product B^T (w X) of both heads, hi then lo, onto what the accumulator holds or in its place.
+__device__ __forceinline__ void issue_state_product(uint32_t tmem, uint32_t b_tile, uint32_t hi_tile, uint32_t lo_tile,
+                                                    bool onto)
+{
+    constexpr uint32_t id_s = bf16_idesc(128, 128, true, true);
+    const uint64_t b = sw128_desc(b_tile, kAtom, 1024);
+    const uint64_t hi = sw128_desc(hi_tile, kAtom, 1024), lo = sw128_desc(lo_tile, kAtom, 1024);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        mma_bf16(tmem + kColS, b + (uint32_t)k * (2048u >> 4), hi + (uint32_t)k * (2048u >> 4), id_s, onto || k > 0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        mma_bf16(tmem + kColS, b + (uint32_t)k * (2048u >> 4), lo + (uint32_t)k * (2048u >> 4), id_s, 1);
+}
+
+// State values of this thread: n = 32 sub + lane, p = 32 hq .. + 31; global
+// layout (p, n), so a warp's lanes are consecutive.
+__device__ __forceinline__ void load_state(const float *src, int r, int hq, float (&v)[32])
 {
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-        st_shared_v4(tile + sw128((uint32_t)r, (uint32_t)(2 * cq + q)), pack_bf16(v[8 * q], v[8 * q + 1]),
+    for (int j = 0; j < 32; ++j) v[j] = src ? __ldcg(src + (32 * hq + j) * kN + r) : 0.f;
+}
+
+__device__ __forceinline__ void store_state(float *dst, int r, int hq, const float (&v)[32])
+{
+#pragma unroll
+    for (int j = 0; j < 32; ++j) __stcg(dst + (32 * hq + j) * kN + r, v[j]);
+}
+
+__device__ __forceinline__ void state_tile(uint32_t tile, int r, int hq, const float (&v)[32])
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        st_shared_v4(tile + sw128((uint32_t)r, (uint32_t)(4 * hq + q)), pack_bf16(v[8 * q], v[8 * q + 1]),
                      pack_bf16(v[8 * q + 2], v[8 * q + 3]), pack_bf16(v[8 * q + 4], v[8 * q + 5]),
                      pack_bf16(v[8 * q + 6], v[8 * q + 7]));
 }
@@ -289,9 +312,25 @@ __device__ __forceinline__ float *seg_state(const SsdPackedParams &p, int64_t pl
     return p.seg_states + (place * p.nheads + h) * (int64_t)(kP * kN);
 }
 
+// Heads h and (nh == 2) h + 1 of group `group`.
+struct Pair {
+    int h, nh, group;
+};
+
+__host__ __device__ __forceinline__ int64_t pairs_of(int64_t nheads, int64_t ngroups)
+{
+    return ngroups * ((nheads / ngroups + 1) / 2);
+}
+
+__device__ __forceinline__ Pair pair_of(const SsdPackedParams &p, int i)
+{
+    const int hpg = (int)(p.nheads / p.ngroups), ppg = (hpg + 1) / 2, group = i / ppg, first = 2 * (i - group * ppg);
+    return {group * hpg + first, min(2, hpg - first), group};
+}
+
 // Set up by all threads: barriers, tensor memory, the segment; false when the
 // CTA has nothing to do (then nothing is allocated).
-__device__ __forceinline__ bool setup(const SsdPackedParams &p, uint8_t *smem, uint32_t base, int64_t place,
+__device__ __forceinline__ bool setup(const SsdPackedParams &p, uint8_t *smem, uint32_t base, int64_t place, int nh,
                                       Segment &g, int &slot, uint32_t &tmem, bool last_too)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -304,19 +343,13 @@ __device__ __forceinline__ bool setup(const SsdPackedParams &p, uint8_t *smem, u
     if (!have) return false;   // (the same for every thread)
     slot = p.state || p.idx ? block_slot(p.idx, g.seq, p.slots) : 0;
     if (slot < 0) return false;
-    auto bar = [&](int i) { return base + kOffBar + 8u * (uint32_t)i; };
     if (threadIdx.x == 0) {
-        mbar_init(bar(kFull), 1);
-        mbar_init(bar(kGFull), 1);
-        mbar_init(bar(kXFull), 1);
-        mbar_init(bar(kWReady), kWarpsC);
-        mbar_init(bar(kMReady), kWarpsC);
-        mbar_init(bar(kSFull), 1);
-        mbar_init(bar(kYFull), 1);
-        mbar_init(bar(kHReady), kWarpsC);
-        mbar_init(bar(kStep0), 32);
-        mbar_init(bar(kStep1), 32);
-        mbar_init(bar(kDrain), 1);
+        auto init = [&](int b, int count) { mbar_init(base + kOffBar + 8u * (uint32_t)b, (uint32_t)count); };
+        for (int b : {kXFull0, kXFull1, kGFull, kSFull, kYFull, kDrain}) init(b, 1);
+        init(kFull, 2);   // B and C
+        for (int b : {kWReady, kMReady, kHReady, kYFree, kYStore0, kYStore1}) init(b, 8 * nh);
+        for (int i = 0; i < 2 * kSteps; ++i) init(kStep0 + i, 32);
+        for (int i = 0; i < kSteps; ++i) init(kSFree0 + i, 1);
         *reinterpret_cast<volatile int *>(smem + kOffMisc + 8) = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -341,156 +374,132 @@ __device__ __forceinline__ void teardown(uint32_t tmem)
 // ---- first kernel: what a segment adds to the state ---------------------------
 // Every segment but a sequence's last (so all its chunks are full): the state
 // at its end, from the sequence's initial state for the first segment and from
-// zero for the others, and its decay. The weights count to the segment's end,
-// so the chunks' products add up without rescaling.
-__global__ void __launch_bounds__(kThreads, 2)
+// zero for the others, and its decay. Chunks run from the segment's end to its
+// start: the decay of what follows a chunk is then a sum that ends at the
+// segment's end, the weights count to there and the chunks' products add up
+// without rescaling. X and B have two buffers (xfull: both landed).
+__global__ void __launch_bounds__(kThreads, 1)
 ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap b_map,
                          const SsdPackedParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = smem_addr(smem);
-    const int64_t place = blockIdx.x / p.nheads;
-    const int h = (int)(blockIdx.x - place * p.nheads);
+    const int pairs = (int)pairs_of(p.nheads, p.ngroups);
+    const int64_t place = blockIdx.x / pairs;
+    const Pair hp = pair_of(p, (int)(blockIdx.x - place * pairs));
     Segment g;
     int slot;
     uint32_t tmem;
-    if (!setup(p, smem, base, place, g, slot, tmem, false)) return;
+    if (!setup(p, smem, base, place, hp.nh, g, slot, tmem, false)) return;
     auto bar = [&](int i) { return base + kOffBar + 8u * (uint32_t)i; };
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);
-    const uint64_t wlim = p.wait_limit_ns;
     StepData *step = reinterpret_cast<StepData *>(smem + kOffStep);
     const int K = (g.len + kQ - 1) / kQ;
-    const int hg = h / (int)(p.nheads / p.ngroups);
-    const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+    const Waiter wait{base + kOffBar, reinterpret_cast<volatile int *>(smem + kOffMisc + 8), p.status, p.wait_limit_ns};
 
-    if (warp == kTmaWarp) {
-        const uint16_t *dtp = reinterpret_cast<const uint16_t *>(p.dt) + (int64_t)g.row * p.dt_st + h;
-        float dtv[4];   // the step inputs of the next chunk (all its tokens are the segment's)
-        load_steps(dtp, p.dt_st, (K - 1) * kQ + 4 * lane, g.len, dtv);
-        // Chunks run from the segment's end to its start: the decay of what follows a
-        // chunk is then a sum that ends at the segment's end.
-        bool ok = true;
-        auto wait = [&](uint32_t b, uint32_t parity) {
-            if (ok) ok = __all_sync(0xffffffffu, wait_for(b, parity, abort_flag, wlim));
-            if (!ok && lane == 0) give_up(p.status, abort_flag);
-            return ok;
-        };
-        auto load_x = [&](int i) {
-            if (lane == 0) {
-                mbar_arrive_tx(bar(kXFull), kAtom);
-                tma_load_2d(base + kOffX, &x_map, bar(kXFull), h * kP, g.row + (K - 1 - i) * kQ);
+    if (warp == kStepWarp || warp == kStepWarp + 1) {
+        const int head = warp - kStepWarp, h = hp.h + head;
+        if (head < hp.nh) {
+            const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+            const uint16_t *dtp = reinterpret_cast<const uint16_t *>(p.dt) + (int64_t)g.row * p.dt_st + h;
+            float dtv[4], after = 0.f;   // the step inputs of the next chunk; decay behind it
+            load_steps(dtp, p.dt_st, (K - 1) * kQ + 4 * lane, g.len, dtv);
+            for (int i = 0; i < K; ++i) {
+                if (i >= kSteps) wait(kSFree0 + step_of(i), step_phase(i - kSteps));
+                float d[4], a[4], pre[4], suf[4], all, w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    d[j] = delta_of(p, dtv[j], bias);
+                    a[j] = log2_decay(d[j], A2);
+                }
+                if (i + 1 < K) load_steps(dtp, p.dt_st, (K - 2 - i) * kQ + 4 * lane, g.len, dtv);
+                token_sums(a, lane, pre, suf, all);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = ex2(suf[j] + after) * d[j];
+                after += all;
+                StepData &st = step[2 * step_of(i) + head];
+                *reinterpret_cast<float4 *>(st.w + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
+                if (lane == 0) st.s[0] = after;
+                mbar_arrive(bar(kStep0 + 2 * step_of(i) + head));
             }
-        };
-        auto load_b = [&](int i) {
-            if (lane == 0) {
-                const int row = g.row + (K - 1 - i) * kQ;
-                mbar_arrive_tx(bar(kFull), 2 * kAtom);
-                tma_load_2d(base + kOffB, &b_map, bar(kFull), hg * kN, row);
-                tma_load_2d(base + kOffB + kAtom, &b_map, bar(kFull), hg * kN + 64, row);
-                if (i + 1 < K) tma_prefetch_2d(&x_map, h * kP, row - kQ);
-            }
-        };
-        float after = 0.f;
-        int xs = 1, bs = 1;   // chunks on their way
-        load_x(0);
-        load_b(0);
+            if (lane == 0) p.seg_decay[place * p.nheads + h] = after;
+        }
+    } else if (warp == kTmaWarp) {
+        int issued = 0;
         for (int i = 0; i < K; ++i) {
-            float d[4], a[4], pre[4], suf[4], all;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                d[j] = delta_of(p, dtv[j], bias);
-                a[j] = log2_decay(d[j], A2);
+            if (i >= 2) wait(kSFree0 + step_of(i - 2), step_phase(i - 2));   // (buffers of chunk i - 2 free)
+            if (lane == 0) {
+                const int row = g.row + (K - 1 - i) * kQ, st = i & 1;
+                const uint32_t full = bar(kXFull0 + st), x = base + kOffX + (uint32_t)(2 * st) * kAtom;
+                const uint32_t b = base + kOffB + (uint32_t)(2 * st) * kAtom;
+                mbar_arrive_tx(full, (uint32_t)(2 + hp.nh) * kAtom);
+                for (int j = 0; j < hp.nh; ++j) tma_load_2d(x + (uint32_t)j * kAtom, &x_map, full, (hp.h + j) * kP, row);
+                tma_load_2d(b, &b_map, full, hp.group * kN, row);
+                tma_load_2d(b + kAtom, &b_map, full, hp.group * kN + 64, row);
             }
-            if (i + 1 < K) load_steps(dtp, p.dt_st, (K - 2 - i) * kQ + 4 * lane, g.len, dtv);
-            token_sums(a, lane, pre, suf, all);
-            float w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = ex2(suf[j] + after) * d[j];
-            after += all;
-            // (the buffer's last reader was chunk i - 2, behind yfull(i - 2))
-            *reinterpret_cast<float4 *>(step[i & 1].w + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
-            if (lane == 0) step[i & 1].s[0] = after;
-            mbar_arrive(bar(kStep0 + (i & 1)));
-            if (i + 1 == K) break;
-            if (!wait(bar(kWReady), i & 1)) break;
-            load_x(i + 1);
-            xs = i + 2;
-            if (!wait(bar(kYFull), i & 1)) break;
-            load_b(i + 1);
-            bs = i + 2;
+            issued = i + 1;
         }
-        if (lane == 0) {
-            p.seg_decay[place * p.nheads + h] = after;
-            mbar_wait(bar(kFull), (bs - 1) & 1);   // loads in flight must land
-            mbar_wait(bar(kXFull), (xs - 1) & 1);
-        }
+        if (lane == 0)   // loads in flight must land
+            for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait(bar(kXFull0 + (i & 1)), (uint32_t)(i >> 1) & 1u);
         __syncwarp();
     } else if (warp == kMmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < K; ++i) {
-                if (!wait_for(bar(kWReady), i & 1, abort_flag, wlim)) {
-                    give_up(p.status, abort_flag);
-                    break;
-                }
-                if (!wait_for(bar(kFull), i & 1, abort_flag, wlim)) {
-                    give_up(p.status, abort_flag);
-                    break;
-                }
+                wait.one(kXFull0 + (i & 1), (uint32_t)(i >> 1) & 1u);
+                wait.one(kWReady, i & 1);
                 tc_after_sync();
-                issue_state_product(tmem, base, i > 0);
-                mma_commit(bar(kYFull));
+                issue_state_product(tmem, base + kOffB + (uint32_t)(2 * (i & 1)) * kAtom, base + kOffW, base + kOffH,
+                                    i > 0);
+                mma_commit(bar(kSFull));
+                mma_commit(bar(kSFree0 + step_of(i)));
             }
-            mma_commit(bar(kDrain));
+            mma_commit(bar(kDrain));   // every MMA must finish before the tensor memory is freed
             mbar_wait(bar(kDrain), 0);
         }
         __syncwarp();
-    } else {
-        const int sub = warp & 3, hq = warp >> 2, r = sub * 32 + lane;
-        const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
-        bool ok = true;
-        auto wait = [&](uint32_t b, uint32_t parity) {
-            if (ok) ok = __all_sync(0xffffffffu, wait_for(b, parity, abort_flag, wlim));
-            if (!ok && lane == 0) give_up(p.status, abort_flag);
-        };
+    } else if ((warp >> 3) < hp.nh) {
+        const int head = warp >> 3, h = hp.h + head, sub = warp & 3, hq = (warp >> 2) & 1, r = sub * 32 + lane;
+        const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16) + kColS + 64u * (uint32_t)head;
         const bool resumed = g.seg == 0 && p.state && p.has_init && p.has_init[g.seq];
         const float *cache = resumed ? p.state + slot * p.s_slot + (int64_t)h * (kP * kN) : nullptr;
         for (int i = 0; i < K; ++i) {
-            wait(bar(kStep0 + (i & 1)), (i >> 1) & 1);
-            wait(bar(kXFull), i & 1);
-            if (i > 0) wait(bar(kYFull), (i - 1) & 1);
-            if (ok) {
-                const float w = step[i & 1].w[r];
+            wait(kStep0 + 2 * step_of(i) + head, step_phase(i));
+            wait(kXFull0 + (i & 1), (uint32_t)(i >> 1) & 1u);
+            if (i > 0) wait(kSFull, (i - 1) & 1);
+            {
+                const float w = step[2 * step_of(i) + head].w[r];
+                const uint32_t x = base + kOffX + (uint32_t)(2 * (i & 1) + head) * kAtom;
 #pragma unroll
-                for (int q = 2 * kCQ * hq; q < 2 * kCQ * (hq + 1); ++q) {
-                    float2 x[4];
-                    widen8(ld_shared_v4(base + kOffX + sw128((uint32_t)r, (uint32_t)q)), x);
-                    store_split(base + kOffC, r, q, x, w);
+                for (int q = 4 * hq; q < 4 * hq + 4; ++q) {
+                    const uint32_t at = (uint32_t)head * kAtom + sw128((uint32_t)r, (uint32_t)q);
+                    uint32_t hi[4], lo[4];
+                    split(ld_shared_v4(x + sw128((uint32_t)r, (uint32_t)q)), w, hi, lo);
+                    st_shared_v4(base + kOffW + at, hi[0], hi[1], hi[2], hi[3]);
+                    st_shared_v4(base + kOffH + at, lo[0], lo[1], lo[2], lo[3]);
                 }
             }
             async_proxy_fence();
             __syncwarp();
-            if (lane == 0 && ok) mbar_arrive(bar(kWReady));
+            if (lane == 0) mbar_arrive(bar(kWReady));
         }
-        wait(bar(kYFull), (K - 1) & 1);
-        if (ok) {
+        wait(kSFull, (K - 1) & 1);
+        {
             tc_after_sync();
-            const float f = ex2(step[(K - 1) & 1].s[0]);
-#pragma unroll 1
-            for (int c = kCQ * hq; c < kCQ * (hq + 1); ++c) {
-                float v[16];
-                tmem_load16(tl + kColS + 16u * c, v);
-                if (cache) {
-                    float v0[16];
-                    load_state(cache, r, c, v0);
-                    // the third kernel's first segment reads the initial state from here: its
-                    // last segment replaces the one in the cache
-                    store_state(seg_state(p, g.base + g.nseg - 1, h), r, c, v0);
+            const float f = ex2(step[2 * step_of(K - 1) + head].s[0]);
+            float v[32];
+            if (cache) {
+                // the third kernel's first segment reads the initial state from its copy: its
+                // last segment replaces the one in the cache
+                load_state(cache, r, hq, v);
+                store_state(seg_state(p, g.base + g.nseg - 1, h), r, hq, v);
+                float t[32];
+                tmem_load32(tl + 32u * hq, t);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = fmaf(f, v0[j], v[j]);
-                }
-                store_state(seg_state(p, place, h), r, c, v);
+                for (int j = 0; j < 32; ++j) v[j] = fmaf(f, v[j], t[j]);
+            } else {
+                tmem_load32(tl + 32u * hq, v);
             }
+            store_state(seg_state(p, place, h), r, hq, v);
         }
     }
     teardown(tmem);
@@ -528,346 +537,373 @@ __global__ void __launch_bounds__(256) ssd_packed_pass_kernel(const SsdPackedPar
 
 // ---- third kernel: outputs and final states ------------------------------------
 
-// M' of row r of the 32-row block `sub`, in place of G: the 16 columns from 16 kk
-// become 8 columns of packed pairs from where they started. In
-// the blocks before the diagonal one the decay is split at the end of the
-// column's block, both factors at most 1 for a decaying state; behind it M' is
-// zero.
-__device__ __forceinline__ void build_mask(uint32_t tg, const StepData &st, int r, int sub, int kk)
+// M' of row r of the 32-row block `sub`: the 32 columns of G of block j <= sub
+// become 16 columns of packed pairs. The decay is split at the end of the
+// column's block: 2^(s_r - s_e) 2^(s_e - s_i). Before the diagonal block both
+// factors are at most 1 for a decaying state. In it the first one grows up to
+// the block's whole decay, which fits a float32 (and its counterpart does not
+// vanish) up to 2^100; stronger decays take the difference itself. (The blocks
+// behind the diagonal are zero, written once.)
+__device__ __forceinline__ void build_mask(uint32_t tg, uint32_t tm, const StepData &st, float sr, int r, int sub, int j)
 {
-    const int i0 = 16 * kk, j = kk >> 1;
-    uint32_t m[8];
-    if (j > sub) {
+    uint32_t m[16];
+    float gv[32];
+    tmem_load32(tg + 32u * (uint32_t)j, gv);
+    const float se = st.s[32 * j + 31];
+    if (j < sub || fabsf(st.s[32 * j] - se) <= 100.f) {
+        const float rf = ex2(sr - se);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m[e] = 0u;
+        for (int e = 0; e < 16; e += 2) {
+            const float4 c = *reinterpret_cast<const float4 *>(st.cf + 32 * j + 2 * e);
+            const float2 a = mul2(f2(gv[2 * e], gv[2 * e + 1]), mul2(f2(rf, rf), f2(c.x, c.y)));
+            const float2 b = mul2(f2(gv[2 * e + 2], gv[2 * e + 3]), mul2(f2(rf, rf), f2(c.z, c.w)));
+            m[e] = pack_bf16(a.x, a.y);
+            m[e + 1] = pack_bf16(b.x, b.y);
+        }
+        if (j == sub) {
+            // row r sees the block's columns up to its own
+            const int seen = r - 32 * j;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                m[e] = 2 * e + 1 <= seen ? m[e] : 2 * e == seen ? m[e] & 0xFFFFu : 0u;
+        }
     } else {
-        const float sr = st.s[r];
-        float gv[16];
-        tmem_load16(tg + (uint32_t)i0, gv);
-        if (j < sub) {
-            const float rf = ex2(sr - st.s[32 * j + 31]);
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const float4 c = *reinterpret_cast<const float4 *>(st.cf + i0 + 2 * e);
-                const float2 a = mul2(f2(gv[2 * e], gv[2 * e + 1]), mul2(f2(rf, rf), f2(c.x, c.y)));
-                const float2 b = mul2(f2(gv[2 * e + 2], gv[2 * e + 3]), mul2(f2(rf, rf), f2(c.z, c.w)));
-                m[e] = pack_bf16(a.x, a.y);
-                m[e + 1] = pack_bf16(b.x, b.y);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const float4 s = *reinterpret_cast<const float4 *>(st.s + i0 + 2 * e);
-                const float4 d = *reinterpret_cast<const float4 *>(st.dl + i0 + 2 * e);
-                const int i = i0 + 2 * e;
-                m[e] = pack_bf16(i <= r ? gv[2 * e] * (ex2(sr - s.x) * d.x) : 0.f,
-                                 i + 1 <= r ? gv[2 * e + 1] * (ex2(sr - s.y) * d.y) : 0.f);
-                m[e + 1] = pack_bf16(i + 2 <= r ? gv[2 * e + 2] * (ex2(sr - s.z) * d.z) : 0.f,
-                                     i + 3 <= r ? gv[2 * e + 3] * (ex2(sr - s.w) * d.w) : 0.f);
-            }
+        for (int e = 0; e < 16; e += 2) {
+            const float4 s = *reinterpret_cast<const float4 *>(st.s + 32 * j + 2 * e);
+            const float4 d = *reinterpret_cast<const float4 *>(st.dl + 32 * j + 2 * e);
+            const int i = 32 * j + 2 * e;
+            m[e] = pack_bf16(i <= r ? gv[2 * e] * (ex2(sr - s.x) * d.x) : 0.f,
+                             i + 1 <= r ? gv[2 * e + 1] * (ex2(sr - s.y) * d.y) : 0.f);
+            m[e + 1] = pack_bf16(i + 2 <= r ? gv[2 * e + 2] * (ex2(sr - s.z) * d.z) : 0.f,
+                                 i + 3 <= r ? gv[2 * e + 3] * (ex2(sr - s.w) * d.w) : 0.f);
         }
     }
-    tmem_store8(tg + (uint32_t)i0, m);
+    tmem_store16(tm + 16u * (uint32_t)j, m);
 }
 
 // GATE: y is multiplied by silu(z) (its own kernel: the code of the loop has to
 // stay small for the instruction cache).
 template <bool GATE>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
 ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap b_map,
-                  const __grid_constant__ CUtensorMap c_map, const SsdPackedParams p)
+                  const __grid_constant__ CUtensorMap c_map, const __grid_constant__ CUtensorMap y_map,
+                  const SsdPackedParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = smem_addr(smem);
-    const int64_t place = blockIdx.x / p.nheads;
-    const int h = (int)(blockIdx.x - place * p.nheads);
+    const int pairs = (int)pairs_of(p.nheads, p.ngroups);
+    const int64_t place = blockIdx.x / pairs;
+    const Pair hp = pair_of(p, (int)(blockIdx.x - place * pairs));
     Segment g;
     int slot;
     uint32_t tmem;
-    if (!setup(p, smem, base, place, g, slot, tmem, true)) return;
+    if (!setup(p, smem, base, place, hp.nh, g, slot, tmem, true)) return;
     auto bar = [&](int i) { return base + kOffBar + 8u * (uint32_t)i; };
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);
-    const uint64_t wlim = p.wait_limit_ns;
     StepData *step = reinterpret_cast<StepData *>(smem + kOffStep);
     const int K = (g.len + kQ - 1) / kQ;
-    const int hg = h / (int)(p.nheads / p.ngroups);
+    const Waiter wait{base + kOffBar, reinterpret_cast<volatile int *>(smem + kOffMisc + 8), p.status, p.wait_limit_ns};
 
-    if (warp == kTmaWarp) {
-        // ---- loads of chunk k, then the step data of chunk k + 1 ----
-        const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-        const uint16_t *dtp = reinterpret_cast<const uint16_t *>(p.dt) + (int64_t)g.row * p.dt_st + h;
-        float dtv[4];   // the step inputs of the chunk whose step data comes next
-        auto load_dt = [&](int k) { load_steps(dtp, p.dt_st, k * kQ + 4 * lane, g.len, dtv); };
-        auto write_step = [&](int k) {
-            float d[4], a[4], pre[4], suf[4], all;
+    if (warp == kStepWarp || warp == kStepWarp + 1) {
+        // ---- step data of one head, up to kSteps chunks ahead ----
+        const int head = warp - kStepWarp, h = hp.h + head;
+        if (head < hp.nh) {
+            const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+            const uint16_t *dtp = reinterpret_cast<const uint16_t *>(p.dt) + (int64_t)g.row * p.dt_st + h;
+            float dtv[4];   // the step inputs of the next chunk
+            load_steps(dtp, p.dt_st, 4 * lane, g.len, dtv);
+            for (int k = 0; k < K; ++k) {
+                if (k >= kSteps) wait(kSFree0 + step_of(k), step_phase(k - kSteps));
+                float d[4], a[4], pre[4], suf[4], all, cf[4], w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = k * kQ + 4 * lane + j;
-                d[j] = t < g.len ? delta_of(p, dtv[j], bias) : 0.f;
-                a[j] = t < g.len ? log2_decay(d[j], A2) : 0.f;
-            }
-            load_dt(k + 1);
-            token_sums(a, lane, pre, suf, all);
-            // running sum at the end of the 32-token block (lanes 8 b .. 8 b + 7 hold block b)
-            const float send = __shfl_sync(0xffffffffu, pre[3], lane | 7);
-            float cf[4], w[4];
+                for (int j = 0; j < 4; ++j) {
+                    const bool in = k * kQ + 4 * lane + j < g.len;
+                    d[j] = in ? delta_of(p, dtv[j], bias) : 0.f;
+                    a[j] = in ? log2_decay(d[j], A2) : 0.f;
+                }
+                load_steps(dtp, p.dt_st, (k + 1) * kQ + 4 * lane, g.len, dtv);
+                token_sums(a, lane, pre, suf, all);
+                // running sum at the end of the 32-token block (lanes 8 b .. 8 b + 7 hold block b)
+                const float send = __shfl_sync(0xffffffffu, pre[3], lane | 7);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                cf[j] = ex2(send - pre[j]) * d[j];
-                w[j] = ex2(suf[j]) * d[j];
+                for (int j = 0; j < 4; ++j) {
+                    cf[j] = ex2(send - pre[j]) * d[j];
+                    w[j] = ex2(suf[j]) * d[j];
+                }
+                StepData &st = step[2 * step_of(k) + head];
+                *reinterpret_cast<float4 *>(st.s + 4 * lane) = make_float4(pre[0], pre[1], pre[2], pre[3]);
+                *reinterpret_cast<float4 *>(st.cf + 4 * lane) = make_float4(cf[0], cf[1], cf[2], cf[3]);
+                *reinterpret_cast<float4 *>(st.dl + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
+                *reinterpret_cast<float4 *>(st.w + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
+                mbar_arrive(bar(kStep0 + 2 * step_of(k) + head));
             }
-            StepData &st = step[k & 1];
-            *reinterpret_cast<float4 *>(st.s + 4 * lane) = make_float4(pre[0], pre[1], pre[2], pre[3]);
-            *reinterpret_cast<float4 *>(st.cf + 4 * lane) = make_float4(cf[0], cf[1], cf[2], cf[3]);
-            *reinterpret_cast<float4 *>(st.dl + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
-            *reinterpret_cast<float4 *>(st.w + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
-            mbar_arrive(bar(kStep0 + (k & 1)));
-        };
-        bool ok = true;
-        auto wait = [&](uint32_t b, uint32_t parity) {
-            if (ok) ok = __all_sync(0xffffffffu, wait_for(b, parity, abort_flag, wlim));
-            if (!ok && lane == 0) give_up(p.status, abort_flag);
-            return ok;
-        };
-        int bc = 0, xs = 0;   // chunks whose B and C, and whose X, are on their way
-        auto load_bc = [&](int k) {
+        }
+    } else if (warp == kTmaWarp) {
+        // ---- loads, each as soon as its buffer was read for the last time ----
+        int cs = 0, xs = 0;   // chunks whose C, and whose X, are on their way
+        auto load_bc = [&](const CUtensorMap *map, uint32_t tile, int k) {
             if (lane == 0) {
-                const int row = g.row + k * kQ;
-                mbar_arrive_tx(bar(kFull), 4 * kAtom);
-                tma_load_2d(base + kOffC, &c_map, bar(kFull), hg * kN, row);
-                tma_load_2d(base + kOffB, &b_map, bar(kFull), hg * kN, row);
-                tma_load_2d(base + kOffC + kAtom, &c_map, bar(kFull), hg * kN + 64, row);
-                tma_load_2d(base + kOffB + kAtom, &b_map, bar(kFull), hg * kN + 64, row);
+                const int row = g.row + k * kQ, col = hp.group * kN;
+                mbar_arrive_tx(bar(kFull), 2 * kAtom);
+                tma_load_2d(tile, map, bar(kFull), col, row);
+                tma_load_2d(tile + kAtom, map, bar(kFull), col + 64, row);
             }
-            bc = k + 1;
+        };
+        // (the wait: its source may be overwritten; the CTA also leaves only after that)
+        auto store_y = [&](int k) {
+            if (lane == 0) {
+                for (int j = 0; j < hp.nh; ++j)
+                    tma_store_2d(&y_map, base + kOffX + (uint32_t)(2 * (k & 1) + j) * kAtom, (hp.h + j) * kP,
+                                 g.row + k * kQ);
+                tma_store_read_wait();
+            }
+            __syncwarp();
         };
         auto load_x = [&](int k) {
             if (lane == 0) {
-                const int row = g.row + k * kQ;
-                mbar_arrive_tx(bar(kXFull), kAtom);
-                tma_load_2d(base + kOffX, &x_map, bar(kXFull), h * kP, row);
-                if (k + 1 < K) tma_prefetch_2d(&x_map, h * kP, row + kQ);
+                const int row = g.row + k * kQ, st = k & 1;
+                mbar_arrive_tx(bar(kXFull0 + st), (uint32_t)hp.nh * kAtom);
+                for (int j = 0; j < hp.nh; ++j)
+                    tma_load_2d(base + kOffX + (uint32_t)(2 * st + j) * kAtom, &x_map, bar(kXFull0 + st),
+                                (hp.h + j) * kP, row);
             }
             xs = k + 1;
         };
-        if (K > 0) {
-            load_bc(0);
-            load_x(0);
-            load_dt(0);
-            write_step(0);
+        for (int k = -1; k + 1 < K; ++k) {
+            if (k >= 0) wait(kGFull, k & 1);
+            load_bc(&c_map, base + kOffC, k + 1);
+            cs = k + 2;
+            if (k >= 0) wait(kSFull, k & 1);
+            load_bc(&b_map, base + kOffB, k + 1);
+            if (k < 0) {
+                load_x(0);
+                if (K > 1) load_x(1);
+            } else {
+                // y of chunk k (a full one) from X's place, then X of chunk k + 2 there
+                wait(kYStore0 + (k & 1), (uint32_t)(k >> 1) & 1u);
+                store_y(k);
+                if (k + 2 < K) load_x(k + 2);
+            }
         }
-        for (int k = 0; k + 1 < K; ++k) {
-            write_step(k + 1);   // (its buffer's last reader was chunk k - 1, behind yfull(k - 1))
-            if (!wait(bar(kSFull), k & 1)) break;
-            load_bc(k + 1);
-            if (!wait(bar(kYFull), k & 1)) break;
-            load_x(k + 1);
+        if (K > 0 && g.len >= K * kQ) {
+            wait(kYStore0 + ((K - 1) & 1), (uint32_t)((K - 1) >> 1) & 1u);
+            store_y(K - 1);
         }
-        if (lane == 0) {   // loads in flight must land
-            if (bc) mbar_wait(bar(kFull), (bc - 1) & 1);
-            if (xs) mbar_wait(bar(kXFull), (xs - 1) & 1);
+        if (lane == 0) {   // loads in flight must land (after a timeout a phase with C but no B runs its limit out)
+            if (cs) mbar_wait(bar(kFull), (uint32_t)(cs - 1) & 1u);
+            for (int k = max(0, xs - 2); k < xs; ++k) mbar_wait(bar(kXFull0 + (k & 1)), (uint32_t)(k >> 1) & 1u);
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ---- MMA issue (one thread) ----
         if (lane == 0) {
             constexpr uint32_t id_g = bf16_idesc(128, 128, false, false);   // G = C B^T
-            constexpr uint32_t id_y = bf16_idesc(128, 64, false, true);     // C H^T and M' X
+            constexpr uint32_t id_o = bf16_idesc(128, 128, false, true);    // C H^T, both heads
+            constexpr uint32_t id_y = bf16_idesc(128, 64, false, true);     // M' X
             const uint64_t dc = sw128_desc(base + kOffC, 16, 1024), db = sw128_desc(base + kOffB, 16, 1024);
             const uint64_t dh = sw128_desc(base + kOffH, kAtom, 1024), dx = sw128_desc(base + kOffX, kAtom, 1024);
-            auto wait = [&](int b, int k) {
-                if (wait_for(bar(b), k & 1, abort_flag, wlim)) return true;
-                give_up(p.status, abort_flag);
-                return false;
-            };
             for (int k = 0; k < K; ++k) {
-                if (!wait(kFull, k) || (k > 0 && !wait(kYFull, k - 1))) break;   // (M' X(k - 1) reads G's columns)
+                // (G(k - 1) was read before mready(k - 1), which the M' X products waited for)
+                wait.one(kFull, k & 1);
                 tc_after_sync();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t off = ((uint32_t)(i >> 2) * kAtom + (uint32_t)(i & 3) * 32u) >> 4;
                     mma_bf16(tmem + kColG, dc + off, db + off, id_g, i > 0);
                 }
-                if (!wait(kHReady, k)) break;
+                wait.one(kHReady, k & 1);
+                if (k > 0) wait.one(kYFree, (k - 1) & 1);
                 tc_after_sync();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t off = ((uint32_t)(i >> 2) * kAtom + (uint32_t)(i & 3) * 32u) >> 4;
-                    mma_bf16(tmem + kColY, dc + off, dh + (uint32_t)i * (2048u >> 4), id_y, i > 0);
+                    mma_bf16(tmem + kColY, dc + off, dh + (uint32_t)i * (2048u >> 4), id_o, i > 0);
                 }
                 mma_commit(bar(kGFull));
-                if (!wait(kWReady, k)) break;
+                wait.one(kWReady, k & 1);
                 tc_after_sync();
-                issue_state_product(tmem, base, true);
+                issue_state_product(tmem, base + kOffB, base + kOffW, base + kOffH, true);
                 mma_commit(bar(kSFull));
-                if (!wait(kMReady, k)) break;
+                wait.one(kMReady, k & 1);
                 tc_after_sync();
+                for (int j = 0; j < hp.nh; ++j) {
+                    const uint64_t dxj = dx + (((uint32_t)(2 * (k & 1) + j) * kAtom) >> 4);
+                    const uint32_t my = tmem + kColY + 64u * (uint32_t)j, mm = tmem + kColM + 64u * (uint32_t)j;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    mma_bf16_ta(tmem + kColY, tmem + kColG + 16u * (uint32_t)i, dx + (uint32_t)i * (2048u >> 4), id_y,
-                                1);
+                    for (int i = 0; i < 8; ++i)
+                        mma_bf16_ta(my, mm + 8u * (uint32_t)i, dxj + (uint32_t)i * (2048u >> 4), id_y, 1);
+                }
                 mma_commit(bar(kYFull));
+                mma_commit(bar(kSFree0 + step_of(k)));
             }
             mma_commit(bar(kDrain));   // every MMA must finish before the tensor memory is freed
             mbar_wait(bar(kDrain), 0);
         }
         __syncwarp();
-    } else {
-        const int sub = warp & 3, hq = warp >> 2, r = sub * 32 + lane;
+    } else if ((warp >> 3) < hp.nh) {
+        const int head = warp >> 3, h = hp.h + head, sub = warp & 3, hq = (warp >> 2) & 1, r = sub * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
-        bool ok = true;
-        auto wait = [&](uint32_t b, uint32_t parity) {
-            if (ok) ok = __all_sync(0xffffffffu, wait_for(b, parity, abort_flag, wlim));
-            if (!ok && lane == 0) give_up(p.status, abort_flag);
-        };
+        const uint32_t ty = tl + kColY + 64u * (uint32_t)head, ts = tl + kColS + 64u * (uint32_t)head;
+        const uint32_t tm = tl + kColM + 64u * (uint32_t)head, htile = base + kOffH + (uint32_t)head * kAtom;
         float *cache = p.state ? p.state + slot * p.s_slot + (int64_t)h * (kP * kN) : nullptr;
         const bool resumed = cache && p.has_init && p.has_init[g.seq];
-        // the state before the segment
         const bool last = cache && g.seg + 1 == g.nseg;
         auto give = [&](int b) {
             async_proxy_fence();
             tc_before_sync();
             __syncwarp();
-            if (lane == 0 && ok) mbar_arrive(bar(b));
+            if (lane == 0) mbar_arrive(bar(b));
         };
         // what a chunk starts from: the state's bf16 tile, and its decayed value in the accumulator
-        auto start = [&](int c, const float (&v)[16], float decay) {
-            state_tile(base + kOffH, r, c, v);
-            tmem_store16_scaled(tl + kColS + 16u * c, v, decay);
-        };
-        if (K > 0) wait(bar(kStep0), 0);
-        const float decay0 = ex2(step[0].s[kQ - 1]);
-#pragma unroll 1
-        for (int c = kCQ * hq; c < kCQ * (hq + 1); ++c) {
-            float v[16];
-            if (g.nseg == 1) {
-                load_state(resumed ? cache : nullptr, r, c, v);
-            } else if (g.seg == 0) {
-                load_state(resumed ? seg_state(p, g.base + g.nseg - 1, h) : nullptr, r, c, v);
-            } else {
-                load_state(seg_state(p, place - 1, h), r, c, v);
+        auto start = [&](float (&v)[32], float decay) {
+            state_tile(htile, r, hq, v);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+                const float2 t = mul2(f2(v[j], v[j + 1]), f2(decay, decay));
+                v[j] = t.x;
+                v[j + 1] = t.y;
             }
+            tmem_store32(ts + 32u * hq, v);
+        };
+        if (K > 0) wait(kStep0 + head, 0);
+        {
+            // the state before the segment
+            const float *from = g.nseg == 1 ? (resumed ? cache : nullptr)
+                                : g.seg > 0 ? seg_state(p, place - 1, h)
+                                            : (resumed ? seg_state(p, g.base + g.nseg - 1, h) : nullptr);
+            float v[32];
+            load_state(from, r, hq, v);
             if (K > 0) {
-                if (ok) start(c, v, decay0);
+                start(v, ex2(step[head].s[kQ - 1]));
             } else if (last && !resumed) {   // an empty sequence leaves the state it starts from
-                store_state(cache, r, c, v);
+                store_state(cache, r, hq, v);
             }
         }
         if (K > 0) {
+            const uint32_t zero[16] = {};
+            for (int j = sub + 1; j < 4; ++j)
+                if ((j & 1) == hq) tmem_store16(tm + 16u * (uint32_t)j, zero);
             tmem_store_wait();
             give(kHReady);
         }
         const float Dh = p.D ? p.D[h] : 0.f;
-        const int64_t col = (int64_t)h * kP + 16 * kCQ * hq;
+        const int64_t col = (int64_t)h * kP + 32 * hq;
         for (int k = 0; k < K; ++k) {
             const bool live = r < g.len - k * kQ;
-            const StepData &st = step[k & 1];
-            wait(bar(kXFull), k & 1);
-            wait(bar(kGFull), k & 1);
-            if (ok) {
-                tc_after_sync();
-                const float er = ex2(st.s[r]), w = st.w[r];
-#pragma unroll 1
-                for (int c = kCQ * hq; c < kCQ * (hq + 1); ++c) {
-                    float y[16];
-                    tmem_load16(tl + kColY + 16u * c, y);
+            const StepData &st = step[2 * step_of(k) + head];
+            const uint32_t xt = base + kOffX + (uint32_t)(2 * (k & 1) + head) * kAtom;
+            wait(kXFull0 + (k & 1), (uint32_t)(k >> 1) & 1u);
+            const float sr = st.s[r];
+            uint32_t lo[4][4] = {};
+            {
+                // w X: the hi term into its tile (free since the last state product), the lo term kept
+                const float w = st.w[r];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint32_t at = base + kOffX + sw128((uint32_t)r, (uint32_t)(2 * c + q));
-                        uint4 xr = ld_shared_v4(at);
-                        if (!live) {
-                            // rows behind the sequence hold other data (any bits): zero where products sum over them
-                            xr = make_uint4(0u, 0u, 0u, 0u);
-                            st_shared_v4(at, 0u, 0u, 0u, 0u);
-                        }
-                        float2 x[4];
-                        widen8(xr, x);
-                        store_split(base + kOffC, r, 2 * c + q, x, w);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = 8 * q + 2 * e;
-                            const float2 t = fma2(f2(er, er), f2(y[j], y[j + 1]), mul2(f2(Dh, Dh), x[e]));
-                            y[j] = t.x;
-                            y[j + 1] = t.y;
-                        }
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t at = sw128((uint32_t)r, (uint32_t)(4 * hq + q));
+                    uint4 xr = ld_shared_v4(xt + at);
+                    if (!live) {
+                        // rows behind the sequence hold other data (any bits): zero where products sum over them
+                        xr = make_uint4(0u, 0u, 0u, 0u);
+                        st_shared_v4(xt + at, 0u, 0u, 0u, 0u);
                     }
-                    tmem_store16(tl + kColY + 16u * c, y);
+                    uint32_t hi[4];
+                    split(xr, w, hi, lo[q]);
+                    st_shared_v4(base + kOffW + (uint32_t)head * kAtom + at, hi[0], hi[1], hi[2], hi[3]);
                 }
-                if (!live) {
+            }
+            wait(kGFull, k & 1);
+            {
 #pragma unroll
-                    for (int i = 0; i < 4 * kCQ; ++i) {
-                        const uint32_t q = (uint32_t)(4 * kCQ * hq + i);
-                        st_shared_v4(base + kOffB + (q >> 3) * kAtom + sw128((uint32_t)r, q & 7u), 0u, 0u, 0u, 0u);
-                    }
+                for (int q = 0; q < 4; ++q)
+                    st_shared_v4(htile + sw128((uint32_t)r, (uint32_t)(4 * hq + q)), lo[q][0], lo[q][1], lo[q][2],
+                                 lo[q][3]);
+                if (!live && head == 0) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        st_shared_v4(base + kOffB + (uint32_t)hq * kAtom + sw128((uint32_t)r, (uint32_t)q), 0u, 0u, 0u,
+                                     0u);
                 }
-                tmem_store_wait();
             }
             give(kWReady);
-            if (ok) {
+            {
+                tc_after_sync();
+                const float er = ex2(sr);
+                float y[32];
+                tmem_load32(ty + 32u * hq, y);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float2 x[4];
+                    widen8(ld_shared_v4(xt + sw128((uint32_t)r, (uint32_t)(4 * hq + q))), x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = 8 * q + 2 * e;
+                        const float2 t = fma2(f2(er, er), f2(y[j], y[j + 1]), mul2(f2(Dh, Dh), x[e]));
+                        y[j] = t.x;
+                        y[j + 1] = t.y;
+                    }
+                }
+                tmem_store32(ty + 32u * hq, y);
 #pragma unroll 1
-                for (int kk = hq; kk < 8; kk += kParts) build_mask(tl + kColG, st, r, sub, kk);
+                for (int j = hq; j <= sub; j += 2) build_mask(tl + kColG, tm, st, sr, r, sub, j);
                 tmem_store_wait();
             }
             give(kMReady);
 
-            wait(bar(kSFull), k & 1);
-            if (k + 1 < K) wait(bar(kStep0 + ((k + 1) & 1)), ((k + 1) >> 1) & 1);
-            if (ok) {
+            wait(kSFull, k & 1);
+            if (k + 1 < K) wait(kStep0 + 2 * step_of(k + 1) + head, step_phase(k + 1));
+            {
                 tc_after_sync();
-                const float decay = ex2(step[(k + 1) & 1].s[kQ - 1]);
-#pragma unroll 1
-                for (int c = kCQ * hq; c < kCQ * (hq + 1); ++c) {
-                    float v[16];
-                    tmem_load16(tl + kColS + 16u * c, v);
-                    if (k + 1 < K) start(c, v, decay);
-                    else if (last) store_state(cache, r, c, v);   // the state after the sequence
-                }
+                float v[32];
+                tmem_load32(ts + 32u * hq, v);
+                if (k + 1 < K) start(v, ex2(step[2 * step_of(k + 1) + head].s[kQ - 1]));
+                else if (last) store_state(cache, r, hq, v);   // the state after the sequence
                 tmem_store_wait();
             }
-            wait(bar(kYFull), k & 1);
-            uint32_t o[8 * kCQ];
-            if (ok) {
+            if (k + 1 < K) give(kHReady);
+            wait(kYFull, k & 1);
+            float y[32] = {};
+            {
                 tc_after_sync();
+                tmem_load32(ty + 32u * hq, y);
+            }
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kYFree));
+            if (live) {
                 const int64_t row = (int64_t)g.row + k * kQ + r;
-                const uint4 *zp = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.z) + row * p.z_st + col);
+                uint32_t o[16];
+                if (GATE) {
+                    const uint4 *zp =
+                        reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.z) + row * p.z_st + col);
 #pragma unroll
-                for (int c = 0; c < kCQ; ++c) {
-                    float y[16];
-                    tmem_load16(tl + kColY + 16u * (kCQ * hq + c), y);
-                    if (GATE && live) {
+                    for (int q = 0; q < 4; ++q) {
+                        float2 z[4];
+                        widen8(__ldg(zp + q), z);
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            float2 z[4];
-                            widen8(__ldg(zp + 2 * c + q), z);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                y[8 * q + 2 * e] *= z[e].x * sigmoid(z[e].x);
-                                y[8 * q + 2 * e + 1] *= z[e].y * sigmoid(z[e].y);
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            y[8 * q + 2 * e] *= z[e].x * sigmoid(z[e].x);
+                            y[8 * q + 2 * e + 1] *= z[e].y * sigmoid(z[e].y);
                         }
                     }
+                }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[8 * c + e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+                for (int e = 0; e < 16; ++e) o[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+                if (g.len >= (k + 1) * kQ) {
+                    // a full chunk: into X's place, from where it is stored as a tile
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        st_shared_v4(xt + sw128((uint32_t)r, (uint32_t)(4 * hq + q)), o[4 * q], o[4 * q + 1],
+                                     o[4 * q + 2], o[4 * q + 3]);
+                } else {
+                    // the sequence's last rows: other sequences' rows follow them
+                    uint4 *yp = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + row * p.y_st + col);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) yp[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                 }
             }
-            if (k + 1 < K) give(kHReady);
-            if (ok && live) {
-                uint16_t *yp = static_cast<uint16_t *>(p.y) + ((int64_t)g.row + k * kQ + r) * p.y_st + col;
-#pragma unroll
-                for (int c = 0; c < kCQ; ++c) {
-                    if (p.y_wide) {
-                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(yp + 16 * c),
-                                     "r"(o[8 * c]), "r"(o[8 * c + 1]), "r"(o[8 * c + 2]), "r"(o[8 * c + 3]),
-                                     "r"(o[8 * c + 4]), "r"(o[8 * c + 5]), "r"(o[8 * c + 6]), "r"(o[8 * c + 7])
-                                     : "memory");
-                    } else {
-                        reinterpret_cast<uint4 *>(yp)[2 * c] = make_uint4(o[8 * c], o[8 * c + 1], o[8 * c + 2], o[8 * c + 3]);
-                        reinterpret_cast<uint4 *>(yp)[2 * c + 1] = 
-                            make_uint4(o[8 * c + 4], o[8 * c + 5], o[8 * c + 6], o[8 * c + 7]);
-                    }
-                }
-            }
+            give(kYStore0 + (k & 1));
         }
     }
     teardown(tmem);
@@ -891,17 +927,17 @@ bool encode_rows(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, i
 }  // namespace
 
 // Chunks per segment (0: sequences are not cut): the smallest estimate of the
-// time, in chunk times of the 2 x num_sms CTAs that run together. n CTAs of at
+// time, in chunk times of the num_sms CTAs that run together. n CTAs of at
 // most c chunks take c when they all run at once, else their work spread over
 // the places plus half a CTA at the end. A CTA's start costs about 0.7 of a
 // chunk; a chunk of the first kernel costs half as much as one of the third,
 // and the additional launches and the pass along the segments about 1 and one
 // thousandth of a chunk for each segment and head.
-int ssd_packed_segment(int64_t tokens, int64_t nseq, int64_t nheads, int64_t max_seqlen, int num_sms)
+int ssd_packed_segment(int64_t tokens, int64_t nseq, int64_t nheads, int64_t ngroups, int64_t max_seqlen, int num_sms)
 {
-    const double slots = 2.0 * (num_sms > 0 ? num_sms : 1);
+    const double slots = num_sms > 0 ? num_sms : 1;
     const int64_t longest = ((max_seqlen > 0 ? min64(max_seqlen, tokens) : tokens) + kQ - 1) / kQ;
-    const double chunks = (double)tokens / kQ + 0.5 * (double)nseq, h = (double)nheads;
+    const double chunks = (double)tokens / kQ + 0.5 * (double)nseq, h = (double)pairs_of(nheads, ngroups);
     const auto spread = [&](double n, double mean, double most) {
         return n <= slots ? most : n * mean / slots + 0.5 * most;
     };
@@ -949,18 +985,17 @@ void ssd_packed_bind(SsdPackedParams &p, void *ws)
     p.seg_states = reinterpret_cast<float *>(static_cast<char *>(ws) + states_offset(places, p.nheads));
 }
 
-cudaError_t launch_ssd_packed(const SsdPackedParams &p0, cudaStream_t stream)
+cudaError_t launch_ssd_packed(const SsdPackedParams &p, cudaStream_t stream)
 {
-    SsdPackedParams p = p0;
-    p.y_wide = reinterpret_cast<uintptr_t>(p.y) % 32 == 0 && p.y_st % 16 == 0;
-    CUtensorMap xm, bm, cm;
+    CUtensorMap xm, bm, cm, ym;
     // (without tokens nothing is loaded; the maps then only need a valid address)
     const int64_t rows = max64(p.tokens, 1);
     const void *none = p.status;
     const int64_t xi = p.nheads * kP, bi = p.ngroups * kN;
     if (!encode_rows(&xm, p.tokens ? p.x : none, xi, rows, p.tokens ? p.x_st : xi) ||
         !encode_rows(&bm, p.tokens ? p.B : none, bi, rows, p.tokens ? p.B_st : bi) ||
-        !encode_rows(&cm, p.tokens ? p.C : none, bi, rows, p.tokens ? p.C_st : bi))
+        !encode_rows(&cm, p.tokens ? p.C : none, bi, rows, p.tokens ? p.C_st : bi) ||
+        !encode_rows(&ym, p.tokens ? p.y : none, xi, rows, p.tokens ? p.y_st : xi))
         return cudaErrorNotSupported;
     const auto kernel = p.z ? ssd_packed_kernel<true> : ssd_packed_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
@@ -969,7 +1004,8 @@ cudaError_t launch_ssd_packed(const SsdPackedParams &p0, cudaStream_t stream)
                                  (int)kSmemBytes);
     if (e == cudaSuccess) e = cudaMemsetAsync(p.status, 0, sizeof(int), stream);
     if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(ssd_packed_places(p.tokens, p.nseq, p.seg_chunks) * p.nheads);
+    const unsigned grid = static_cast<unsigned>(ssd_packed_places(p.tokens, p.nseq, p.seg_chunks) *
+                                                pairs_of(p.nheads, p.ngroups));
     if (p.seg_chunks) {
         ssd_packed_states_kernel<<<grid, kThreads, kSmemBytes, stream>>>(xm, bm, p);
         e = cudaGetLastError();
@@ -978,7 +1014,7 @@ cudaError_t launch_ssd_packed(const SsdPackedParams &p0, cudaStream_t stream)
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    kernel<<<grid, kThreads, kSmemBytes, stream>>>(xm, bm, cm, p);
+    kernel<<<grid, kThreads, kSmemBytes, stream>>>(xm, bm, cm, ym, p);
     return cudaGetLastError();
 }
 
