@@ -815,343 +815,18 @@ def ssd_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, init
 
 
 # ----------------------------------------------------------------------------
-# Mamba-2 serving (packed sequences, states in cache slots) and norms
+# Mamba-2 serving operators and norms (serving.py, loaded with torch on first use)
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+_SERVING = ("conv_packed_fwd", "conv_packed_update", "ssd_packed_fwd", "ssd_state_update", "norm_fwd", "norm_bwd")
 
 
-def _call(device, fn, *args, stream=None):
-    """Run a library call that ends in a stream argument, on ``stream`` or the
-    current stream of ``device``, with ``device`` current."""
-    torch = _torch()
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, (stream or torch.cuda.current_stream(device)).cuda_stream))
-    else:
-        with torch.cuda.device(device):
-            _check(fn(*args, (stream or torch.cuda.current_stream(device)).cuda_stream))
-
-
-def _need_slots(nseq, state, state_indices, has_initial_state):
-    torch = _torch()
-    _need_cuda("state_indices", state_indices, torch.int32, 1)
-    if state_indices is not None and (tuple(state_indices.shape) != (nseq,) or not state_indices.is_contiguous()):
-        raise ValueError(f"state_indices must be a contiguous ({nseq},) int32 tensor")
-    if has_initial_state is not None:
-        _need_cuda("has_initial_state", has_initial_state, None, 1)
-        if (has_initial_state.dtype not in (torch.bool, torch.uint8) or tuple(has_initial_state.shape) != (nseq,)
-                or not has_initial_state.is_contiguous()):
-            raise ValueError(f"has_initial_state must be a contiguous ({nseq},) bool or uint8 tensor")
-
-
-def _need_cu_seqlens(cu_seqlens):
-    _need_cuda("cu_seqlens", cu_seqlens, _torch().int32, 1)
-    if cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens must be a contiguous int32 tensor of nseq + 1 values")
-    return cu_seqlens.numel() - 1
-
-
-def _conv_packed(x, weight, bias, silu, cu_seqlens, nseq, state, state_indices, has_initial_state, out, stream):
-    _need_cuda("x", x, None, 2)
-    tokens, channels = x.shape
-    y = _torch().empty((tokens, channels), dtype=x.dtype, device=x.device) if out is None else out
-    _need_cuda("out", y, x.dtype, 2)
-    if tuple(y.shape) != (tokens, channels):
-        raise ValueError(f"out must have shape {(tokens, channels)}")
-    conv = build_conv_args(weight, bias, silu)
-    if weight.shape[0] != channels:
-        raise ValueError("conv weight must have one row per channel")
-    _need_slots(nseq, state, state_indices, has_initial_state)
-    a = ConvPackedArgs()
-    if state is not None:
-        _need_cuda("state", state, x.dtype, 3)
-        if tuple(state.shape[1:]) != (conv.width - 1, channels):
-            raise ValueError(f"state must be (slots, {conv.width - 1}, {channels})")
-        a.slots, a.state = state.shape[0], _ptr(state)
-        a.state_slot_stride, a.state_row_stride = state.stride(0), max(state.stride(1), channels)
-    _same_device(x.device, weight=weight, bias=bias, cu_seqlens=cu_seqlens, state=state, state_indices=state_indices,
-                 has_initial_state=has_initial_state, out=y)
-    a.tokens, a.channels, a.nseq = tokens, channels, nseq
-    a.in_dtype = _dtype_code(x)
-    a.x, a.x_token_stride = _ptr(x), x.stride(0)
-    a.y, a.y_token_stride = _ptr(y), max(y.stride(0), channels) if tokens <= 1 else y.stride(0)
-    a.cu_seqlens, a.state_indices = _ptr(cu_seqlens), _ptr(state_indices)
-    a.has_initial_state = _ptr(has_initial_state)
-    _call(x.device, load_library().mamba_conv_packed_fwd, ctypes.byref(a), ctypes.byref(conv), stream=stream)
-    return y
-
-
-def conv_packed_fwd(x, weight, cu_seqlens, bias=None, silu=True, state=None, state_indices=None,
-                    has_initial_state=None, out=None, stream=None):
-    """Causal depthwise convolution (and SiLU) over packed sequences.
-
-    ``x`` (tokens, channels) float32 or bfloat16, channels contiguous: the
-    sequences' tokens one behind the other, sequence s in rows
-    ``cu_seqlens[s]`` to ``cu_seqlens[s + 1]`` (int32, nseq + 1 values on the
-    device). ``weight`` (channels, width <= 4) and ``bias`` (channels,)
-    float32. ``state`` (slots, width - 1, channels) in x's dtype holds each
-    request's last width - 1 inputs, oldest first, and is updated in place:
-    sequence s uses slot ``state_indices[s]`` (int32; None: slot s) and
-    continues from it where ``has_initial_state[s]`` (bool; None: nowhere).
-    Sequences with an index outside the cache, or an earlier sequence's, are
-    skipped: their rows of the output and the cache stay as they were. Returns
-    y (tokens, channels); rows of no sequence are not written.
-    """
-    nseq = _need_cu_seqlens(cu_seqlens)
-    return _conv_packed(x, weight, bias, silu, cu_seqlens, nseq, state, state_indices, has_initial_state, out, stream)
-
-
-def conv_packed_update(state, x, weight, bias=None, silu=True, state_indices=None, out=None, stream=None):
-    """The same for one token per request: ``x`` (batch, channels), row b
-    continuing from slot ``state_indices[b]`` (None: slot b) of ``state``,
-    which takes the token in place. Skipped rows as :func:`conv_packed_fwd`."""
-    return _conv_packed(x, weight, bias, silu, None, x.shape[0], state, state_indices, None, out, stream)
-
-
-def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_softplus=True, state=None,
-                   state_indices=None, has_initial_state=None, max_seqlen=0, out=None, workspace=None, check=True,
-                   stream=None, wait_limit_us=0):
-    """Mamba-2 scalar-decay SSM over packed sequences (chunked SSD on the tensor cores).
-
-    The recurrence of :func:`ssd_fwd` for sequences packed one behind the
-    other: x, z (tokens, nheads, 64), dt (tokens, nheads), B, C (tokens,
-    ngroups, 128) bfloat16, the axes behind the tokens contiguous (slices of a
-    wider row are fine); A, D, dt_bias (nheads,) float32. ``cu_seqlens``,
-    ``state_indices`` and ``has_initial_state`` as :func:`conv_packed_fwd`;
-    ``state`` (slots, nheads, 64, 128) float32 is updated in place (None:
-    every sequence starts from zero and leaves no state). ``max_seqlen``: the
-    longest sequence if the host knows it; it steers the schedule only.
-    Returns y (tokens, nheads, 64); rows of no or of a skipped sequence are not
-    written. ``workspace``: a uint8 CUDA tensor, allocated here when None or too
-    small. With ``check`` the call synchronizes the stream and raises if the
-    kernel reported a failed wait; without it, pass a workspace and call
-    :func:`ssd_check` on it later.
-    """
-    torch = _torch()
-    _need_cuda("x", x, None, 3)
-    tokens, nheads = x.shape[0], x.shape[1]
-    nseq = _need_cu_seqlens(cu_seqlens)
-    y = torch.empty((tokens, nheads, SSD_HEADDIM), dtype=x.dtype, device=x.device) if out is None else out
-    _need_cuda("B", B, x.dtype, 3)
-    ngroups = B.shape[1]
-    for name, t, shape in (("x", x, (tokens, nheads, SSD_HEADDIM)), ("out", y, (tokens, nheads, SSD_HEADDIM)),
-                           ("z", z, (tokens, nheads, SSD_HEADDIM)), ("dt", dt, (tokens, nheads)),
-                           ("B", B, (tokens, ngroups, SSD_DSTATE)), ("C", C, (tokens, ngroups, SSD_DSTATE))):
-        _need_rows(name, t, x.dtype, shape)
-    for name, t in (("A", A), ("D", D), ("dt_bias", dt_bias)):
-        _need_heads(name, t, nheads)
-    _need_slots(nseq, state, state_indices, has_initial_state)
-    a = SsdPackedArgs()
-    if state is not None:
-        _need_cuda("state", state, torch.float32, 4)
-        if tuple(state.shape[1:]) != (nheads, SSD_HEADDIM, SSD_DSTATE) or not state[:1].is_contiguous():
-            raise ValueError(f"state must be (slots, {nheads}, 64, 128) float32, contiguous behind the slots")
-        a.slots, a.state, a.state_slot_stride = state.shape[0], _ptr(state), state.stride(0)
-    _same_device(x.device, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, cu_seqlens=cu_seqlens, state=state,
-                 state_indices=state_indices, has_initial_state=has_initial_state, out=y, workspace=workspace)
-    a.tokens, a.nseq, a.nheads, a.ngroups, a.max_seqlen = tokens, nseq, nheads, ngroups, int(max_seqlen)
-    a.in_dtype, a.dt_softplus = _dtype_code(x), 1 if dt_softplus else 0
-    for name, t in (("x", x), ("dt", dt), ("B", B), ("C", C), ("z", z), ("y", y)):
-        if t is not None:
-            setattr(a, name, _ptr(t))
-            setattr(a, f"{name}_token_stride", t.stride(0) if tokens > 1 else t.shape[1:].numel())
-    a.A, a.D, a.dt_bias = _ptr(A), _ptr(D), _ptr(dt_bias)
-    a.cu_seqlens, a.state_indices, a.has_initial_state = _ptr(cu_seqlens), _ptr(state_indices), _ptr(has_initial_state)
-    a.wait_limit_us = int(wait_limit_us)
-    lib = load_library()
-    n = _workspace_bytes(x.device, lib.mamba_ssd_packed_workspace_size, a)
-    own_ws = workspace is None or workspace.numel() < n
-    if own_ws:
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
-    _call(x.device, lib.mamba_ssd_packed_fwd, ctypes.byref(a), workspace.data_ptr(), workspace.numel(), stream=stream)
-    if own_ws:
-        _keep_until_done(workspace, stream)
-    if check:
-        ssd_check(workspace, stream)
-    return y
-
-
-def ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, state_indices=None,
-                     out=None, stream=None):
-    """One Mamba-2 decode step for a batch of requests, states in cache slots.
-
-    ``state`` (slots, nheads, headdim, dstate) float32 is updated in place, row
-    b in slot ``state_indices[b]`` (int32; None: slot b); x, z (batch, nheads,
-    headdim), dt (batch, nheads), B, C (batch, ngroups, dstate) all float32 or
-    all bfloat16, the axes behind the batch contiguous; A, D, dt_bias
-    (nheads,) float32. Any headdim, dstate up to 256. Returns y (batch,
-    nheads, headdim); rows whose index lies outside the cache, or is an earlier
-    row's, are skipped (output row and cache stay as they were).
-    """
-    torch = _torch()
-    _need_cuda("x", x, None, 3)
-    batch, nheads, headdim = x.shape
-    y = torch.empty((batch, nheads, headdim), dtype=x.dtype, device=x.device) if out is None else out
-    _need_cuda("B", B, x.dtype, 3)
-    ngroups, dstate = B.shape[1], B.shape[2]
-    for name, t, shape in (("x", x, (batch, nheads, headdim)), ("out", y, (batch, nheads, headdim)),
-                           ("z", z, (batch, nheads, headdim)), ("dt", dt, (batch, nheads)),
-                           ("B", B, (batch, ngroups, dstate)), ("C", C, (batch, ngroups, dstate))):
-        _need_rows(name, t, x.dtype, shape)
-    _need_cuda("state", state, torch.float32, 4)
-    if tuple(state.shape[1:]) != (nheads, headdim, dstate) or not state[:1].is_contiguous():
-        raise ValueError(f"state must be (slots, {nheads}, {headdim}, {dstate}) float32, contiguous behind the slots")
-    for name, t in (("A", A), ("D", D), ("dt_bias", dt_bias)):
-        _need_heads(name, t, nheads)
-    _need_slots(batch, state, state_indices, None)
-    _same_device(x.device, state=state, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, state_indices=state_indices,
-                 out=y)
-    a = SsdUpdateArgs()
-    a.batch, a.nheads, a.ngroups, a.headdim, a.dstate, a.slots = batch, nheads, ngroups, headdim, dstate, state.shape[0]
-    a.in_dtype, a.dt_softplus = _dtype_code(x), 1 if dt_softplus else 0
-    a.state, a.state_slot_stride = _ptr(state), state.stride(0)
-    a.x, a.x_batch_stride = _ptr(x), x.stride(0)
-    a.dt, a.dt_batch_stride = _ptr(dt), dt.stride(0)
-    a.B, a.B_batch_stride = _ptr(B), B.stride(0)
-    a.C, a.C_batch_stride = _ptr(C), C.stride(0)
-    if z is not None:
-        a.z, a.z_batch_stride = _ptr(z), z.stride(0)
-    a.y, a.y_batch_stride = _ptr(y), y.stride(0)
-    a.A, a.D, a.dt_bias, a.state_indices = _ptr(A), _ptr(D), _ptr(dt_bias), _ptr(state_indices)
-    _call(x.device, load_library().mamba_ssd_state_update, ctypes.byref(a), stream=stream)
-    return y
-
-
-def _need_heads(name, t, nheads):
-    _need_cuda(name, t, _torch().float32, 1)
-    if t is not None and (tuple(t.shape) != (nheads,) or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous ({nheads},) float32 tensor")
-
-
-def _need_rows(name, t, dtype, shape):
-    """A tensor of this dtype and shape whose axes behind the first are contiguous."""
-    if t is None:
-        return
-    _need_cuda(name, t, dtype, len(shape))
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    want = 1
-    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n > 1 and st != want:
-            raise ValueError(f"{name} must be contiguous behind its first axis")
-        want *= n
-
-
-def _norm_args(x, weight, z, residual_like, residual_scale, eps, group_size, gate_first):
-    """The fields of ``ms_norm_args`` that the forward and the backward share."""
-    torch = _torch()
-    _need_cuda("x", x, None, 2)
-    rows, dim = x.shape
-    _need_rows("z", z, x.dtype, (rows, dim))
-    _need_cuda("weight", weight, torch.float32, 1)
-    if weight is not None and (tuple(weight.shape) != (dim,) or not weight.is_contiguous()):
-        raise ValueError(f"weight must be a contiguous ({dim},) float32 tensor")
-    a = NormArgs()
-    a.rows, a.dim, a.group_size = rows, dim, dim if group_size is None else int(group_size)
-    a.in_dtype = _dtype_code(x)
-    a.residual_dtype = a.in_dtype
-    if residual_like is not None:
-        if residual_like.dtype not in (x.dtype, torch.float32):
-            raise TypeError(f"the residual must be {x.dtype} or float32, got {residual_like.dtype}")
-        a.residual_dtype = _dtype_code(residual_like)
-    a.eps, a.residual_scale, a.gate_first = eps, residual_scale, 1 if gate_first else 0
-    a.x, a.x_row_stride = _ptr(x), x.stride(0)
-    if z is not None:
-        a.z, a.z_row_stride = _ptr(z), z.stride(0)
-    a.weight = _ptr(weight)
-    return a
-
-
-def norm_fwd(x, weight=None, z=None, residual=None, residual_scale=1.0, eps=1e-5, group_size=None, gate_first=True,
-             out=None, residual_out=None, stream=None):
-    """RMS norm of each row's groups of ``group_size`` channels (None: the row).
-
-    v = x, or x * silu(z) with ``z`` and ``gate_first``; with ``residual``
-    v = residual + residual_scale * v, which is also returned (in residual's
-    dtype, x's or float32); y = v / sqrt(mean(v^2) + eps) * weight, times
-    silu(z) when the gate comes last. x, z (rows, dim) float32 or bfloat16,
-    rows of any stride; weight (dim,) float32 or None. Returns ``(y,
-    residual_out)``, residual_out None without a residual.
-    """
-    torch = _torch()
-    a = _norm_args(x, weight, z, residual, residual_scale, eps, group_size, gate_first)
-    shape = tuple(x.shape)
-    y = torch.empty(shape, dtype=x.dtype, device=x.device) if out is None else out
-    _need_rows("out", y, x.dtype, shape)
-    if residual is not None:
-        _need_rows("residual", residual, residual.dtype, shape)
-        if residual_out is None:
-            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
-        _need_rows("residual_out", residual_out, residual.dtype, shape)
-        a.residual, a.residual_row_stride = _ptr(residual), residual.stride(0)
-        a.residual_out, a.residual_out_row_stride = _ptr(residual_out), residual_out.stride(0)
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    _same_device(x.device, weight=weight, z=z, residual=residual, out=y, residual_out=residual_out)
-    a.y, a.y_row_stride = _ptr(y), y.stride(0)
-    _call(x.device, load_library().mamba_norm_fwd, ctypes.byref(a), stream=stream)
-    return y, residual_out
-
-
-def norm_bwd(dy, x, weight=None, z=None, residual_out=None, dresidual_out=None, residual_scale=1.0, eps=1e-5,
-             group_size=None, gate_first=True, workspace=None, stream=None):
-    """Gradients of :func:`norm_fwd` for the loss sum(y * dy) + sum(residual_out * dresidual_out).
-
-    ``residual_out`` is the sum that the forward returned (None: it had no
-    residual); ``dresidual_out``, in its dtype, may be None. Returns a dict:
-    dx, dz (None without z) in x's dtype, dresidual (None without a residual)
-    in the residual's, dweight (dim,) float32 (None without weight).
-    ``workspace``: optional uint8 CUDA tensor, allocated here when needed.
-    """
-    torch = _torch()
-    a = _norm_args(x, weight, z, residual_out, residual_scale, eps, group_size, gate_first)
-    shape = tuple(x.shape)
-    _need_rows("dy", dy, x.dtype, shape)
-    if residual_out is None and dresidual_out is not None:
-        raise ValueError("dresidual_out needs residual_out")
-    g = NormBwdArgs()
-    out = {"dx": torch.empty(shape, dtype=x.dtype, device=x.device), "dz": None, "dresidual": None, "dweight": None}
-    if z is not None:
-        out["dz"] = torch.empty(shape, dtype=x.dtype, device=x.device)
-        g.dz, g.dz_row_stride = _ptr(out["dz"]), shape[1]
-    if residual_out is not None:
-        _need_rows("residual_out", residual_out, residual_out.dtype, shape)
-        _need_rows("dresidual_out", dresidual_out, residual_out.dtype, shape)
-        a.residual_out, a.residual_out_row_stride = _ptr(residual_out), residual_out.stride(0)
-        out["dresidual"] = torch.empty(shape, dtype=residual_out.dtype, device=x.device)
-        g.dresidual, g.dresidual_row_stride = _ptr(out["dresidual"]), shape[1]
-        if dresidual_out is not None:
-            g.dresidual_out, g.dresidual_out_row_stride = _ptr(dresidual_out), dresidual_out.stride(0)
-    if weight is not None:
-        out["dweight"] = torch.empty(shape[1], dtype=torch.float32, device=x.device)
-        g.dweight = _ptr(out["dweight"])
-    _same_device(x.device, dy=dy, weight=weight, z=z, residual_out=residual_out, dresidual_out=dresidual_out,
-                 workspace=workspace)
-    g.dy, g.dy_row_stride = _ptr(dy), dy.stride(0)
-    g.dx, g.dx_row_stride = _ptr(out["dx"]), shape[1]
-    lib = load_library()
-    own_ws, n = False, 0
-    if weight is not None:
-        n = _workspace_bytes(x.device, lib.mamba_norm_bwd_workspace_size, a)
-        own_ws = n > 0 and (workspace is None or workspace.numel() < n)
-        if own_ws:
-            workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
-    _call(x.device, lib.mamba_norm_bwd, ctypes.byref(a), ctypes.byref(g), _ptr(workspace),
-          0 if workspace is None else workspace.numel(), stream=stream)
-    if own_ws:
-        _keep_until_done(workspace, stream)
-    return out
-
-
-def _workspace_bytes(device, fn, args):
-    """Bytes that a workspace query reports for ``args`` with ``device`` current."""
-    torch = _torch()
-    n = ctypes.c_size_t(0)
-    with torch.cuda.device(device):
-        _check(fn(ctypes.byref(args), ctypes.byref(n)))
-    return n.value
+def __getattr__(name):
+    if name in _SERVING:
+        from . import serving
+        for n in _SERVING:
+            globals()[n] = getattr(serving, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 PROBE_UNITS = {"ex2": 0, "tanh": 1, "ffma": 2, "ffma2": 3}

@@ -1,0 +1,387 @@
+"""Mamba-2 serving operators and norms: packed sequences, states in cache slots.
+
+The calls that a serving step makes for every layer: on small batches they are
+bound by the host, so this module marshals lean. Arguments are checked once and
+packed into the C structs of ``include/mambascan.h`` with :mod:`struct`; the
+structs' ctypes mirrors (``ConvPackedArgs`` and so on) describe the same
+layouts. Outputs are allocated here unless ``out`` is given.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+from . import (MS_BF16, MS_F32, SSD_DSTATE, SSD_HEADDIM, MambaScanError, load_library, ssd_check)
+
+# struct layouts, field by field as in the header (P: pointer, q: int64, i: int32, f: float, B: uint8)
+CONV_PACKED = struct.Struct("@4q2i Pq Pq Pqq PPP")
+CONV1D = struct.Struct("@PPii")
+SSD_PACKED = struct.Struct("@6q2i Pq Pq Pq Pq Pq Pq PPP Pq PPP Ii")
+SSD_UPDATE = struct.Struct("@6q2i Pq Pq Pq Pq Pq Pq Pq PPPP")
+NORM = struct.Struct("@3q2i2f2i Pq Pq Pq Pq Pq P")
+NORM_BWD = struct.Struct("@Pq Pq Pq Pq Pq P")
+
+_DTYPES = {torch.float32: MS_F32, torch.bfloat16: MS_BF16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_fns = {}
+
+
+def _fn(name, *argtypes):
+    """An entry point that takes its structs as bytes (a function object of its own)."""
+    f = _fns.get(name)
+    if f is None:
+        f = load_library()[name]
+        f.restype = ctypes.c_int
+        f.argtypes = argtypes
+        _fns[name] = f
+    return f
+
+
+_str, _ptr, _size = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t
+
+
+def _run(device, stream, fn, *args):
+    """``fn(*args, stream)`` with ``device`` current, on ``stream`` or the device's current stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _run(device, stream, fn, *args)
+    if stream is not None:
+        s = stream.cuda_stream
+    elif _raw_stream is not None:
+        s = _raw_stream(device.index)
+    else:
+        s = torch.cuda.current_stream(device).cuda_stream
+    status = fn(*args, s)
+    if status:
+        raise MambaScanError(status, load_library().mamba_last_error().decode(errors="replace"))
+
+
+def _workspace_bytes(device, name, args):
+    """Bytes that a workspace query reports for the packed ``args`` on ``device``."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _workspace_bytes(device, name, args)
+    n = _size(0)
+    status = _fn(name, _str, ctypes.POINTER(_size))(args, ctypes.byref(n))
+    if status:
+        raise MambaScanError(status, load_library().mamba_last_error().decode(errors="replace"))
+    return n.value
+
+
+def _workspace(device, workspace, need):
+    """(tensor, whether it was allocated here) of at least ``need`` bytes."""
+    if workspace is not None:
+        if workspace.dtype is not torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+        if workspace.numel() >= need:
+            return workspace, False
+    return torch.empty(need, dtype=torch.uint8, device=device), True
+
+
+def _keep(t, stream):
+    """Scratch allocated on the current stream but used on ``stream``."""
+    if stream is not None:
+        t.record_stream(stream)
+
+
+def _cuda(x, ndim, what):
+    """Device and dtype code of the leading tensor of a call."""
+    if not x.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if x.dim() != ndim:
+        raise ValueError(f"{what} must have {ndim} dimensions")
+    code = _DTYPES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {x.dtype} (float32 or bfloat16)")
+    return x.device, code
+
+
+def _refuse(name, t, dtype, shape, device):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows(name, t, dtype, shape, device):
+    """(pointer, stride of the first axis) of a tensor whose axes behind the first are contiguous."""
+    if t is None:
+        return 0, 0
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        _refuse(name, t, dtype, shape, device)
+    stride = t.stride()
+    if shape[0] <= 1 or not t.is_contiguous():
+        inner = 1
+        for n, st in zip(reversed(shape[1:]), reversed(stride[1:])):
+            if n > 1 and st != inner:
+                raise ValueError(f"{name} must be contiguous behind its first axis")
+            inner *= n
+        if shape[0] <= 1:
+            return t.data_ptr(), inner
+    return t.data_ptr(), stride[0]
+
+
+def _vector(name, t, n, device, dtype=torch.float32):
+    """Pointer of a contiguous vector of n values (0 for None)."""
+    if t is None:
+        return 0
+    if t.shape != (n,) or t.dtype is not dtype or t.device != device:
+        _refuse(name, t, dtype, (n,), device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _slots(nseq, state_indices, has_initial_state, device):
+    """Pointers of the index table and the flags."""
+    flags = 0
+    if has_initial_state is not None:
+        kind = torch.uint8 if has_initial_state.dtype is torch.uint8 else torch.bool
+        flags = _vector("has_initial_state", has_initial_state, nseq, device, kind)
+    return _vector("state_indices", state_indices, nseq, device, torch.int32), flags
+
+
+def _offsets(cu_seqlens, device):
+    """(pointer, number of sequences) of the row offsets."""
+    n = cu_seqlens.numel()
+    if n < 1:
+        raise ValueError("cu_seqlens must hold nseq + 1 values")
+    return _vector("cu_seqlens", cu_seqlens, n, device, torch.int32), n - 1
+
+
+# ---- convolution ---------------------------------------------------------------
+
+def _conv(x, weight, bias, silu, cu, nseq, state, state_indices, has_initial_state, out, stream):
+    device, code = _cuda(x, 2, "x")
+    tokens, channels = shape = x.shape
+    y = x.new_empty(shape) if out is None else out
+    if weight.dim() != 2:
+        raise ValueError("conv weight must be (channels, width)")
+    width = weight.shape[1]
+    if weight.shape[0] != channels or not weight.is_contiguous():
+        raise ValueError("conv weight must be contiguous with one row per channel")
+    if weight.dtype is not torch.float32 or weight.device != device:
+        _refuse("conv weight", weight, torch.float32, (channels, width), device)
+    idx, flags = _slots(nseq, state_indices, has_initial_state, device)
+    st = slot_stride = row_stride = slots = 0
+    if state is not None:
+        slots = state.shape[0] if state.dim() == 3 else -1
+        if state.shape != (slots, width - 1, channels) or state.dtype is not x.dtype or state.device != device:
+            _refuse("state", state, x.dtype, ("slots", width - 1, channels), device)
+        slot_stride, row_stride, last = state.stride()
+        if last != 1 and channels > 1:
+            raise ValueError("state must be contiguous along the channels")
+        if width <= 2:
+            row_stride = max(row_stride, channels)   # (one row per slot: its stride is not used)
+        st = state.data_ptr()
+    xp, xs = _rows("x", x, x.dtype, shape, device)
+    yp, ys = _rows("out", y, x.dtype, shape, device)
+    args = CONV_PACKED.pack(tokens, channels, nseq, slots, code, 0, xp, xs, yp, ys, st, slot_stride, row_stride,
+                            cu, idx, flags)
+    conv = CONV1D.pack(weight.data_ptr(), _vector("conv bias", bias, channels, device), width, 1 if silu else 0)
+    _run(device, stream, _fn("mamba_conv_packed_fwd", _str, _str, _ptr), args, conv)
+    return y
+
+
+def conv_packed_fwd(x, weight, cu_seqlens, bias=None, silu=True, state=None, state_indices=None,
+                    has_initial_state=None, out=None, stream=None):
+    """Causal depthwise convolution (and SiLU) over packed sequences.
+
+    ``x`` (tokens, channels) float32 or bfloat16, channels contiguous: the
+    sequences' tokens one behind the other, sequence s in rows
+    ``cu_seqlens[s]`` to ``cu_seqlens[s + 1]`` (int32, nseq + 1 values on the
+    device). ``weight`` (channels, width <= 4) and ``bias`` (channels,)
+    float32. ``state`` (slots, width - 1, channels) in x's dtype holds each
+    request's last width - 1 inputs, oldest first, and is updated in place:
+    sequence s uses slot ``state_indices[s]`` (int32; None: slot s) and
+    continues from it where ``has_initial_state[s]`` (bool; None: nowhere).
+    Sequences with an index outside the cache, or an earlier sequence's, are
+    skipped: their rows of the output and the cache stay as they were. Returns
+    y (tokens, channels); rows of no sequence are not written.
+    """
+    cu, nseq = _offsets(cu_seqlens, x.device)
+    return _conv(x, weight, bias, silu, cu, nseq, state, state_indices, has_initial_state, out, stream)
+
+
+def conv_packed_update(state, x, weight, bias=None, silu=True, state_indices=None, out=None, stream=None):
+    """The same for one token per request: ``x`` (batch, channels), row b
+    continuing from slot ``state_indices[b]`` (None: slot b) of ``state``,
+    which takes the token in place. Skipped rows as :func:`conv_packed_fwd`."""
+    return _conv(x, weight, bias, silu, 0, x.shape[0], state, state_indices, None, out, stream)
+
+
+# ---- SSD -----------------------------------------------------------------------
+
+def _ssd_state(state, nheads, headdim, dstate, device):
+    """(slots, pointer, slot stride) of a cache of float32 states."""
+    slots = state.shape[0] if state.dim() == 4 else -1
+    shape = (slots, nheads, headdim, dstate)
+    if state.shape != shape or state.dtype is not torch.float32 or state.device != device:
+        _refuse("state", state, torch.float32, ("slots", nheads, headdim, dstate), device)
+    ptr, stride = _rows("state", state, torch.float32, shape, device)
+    return slots, ptr, stride
+
+
+def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_softplus=True, state=None,
+                   state_indices=None, has_initial_state=None, max_seqlen=0, out=None, workspace=None, check=True,
+                   stream=None, wait_limit_us=0):
+    """Mamba-2 scalar-decay SSM over packed sequences (chunked SSD on the tensor cores).
+
+    The recurrence of :func:`ssd_fwd` for sequences packed one behind the
+    other: x, z (tokens, nheads, 64), dt (tokens, nheads), B, C (tokens,
+    ngroups, 128) bfloat16, the axes behind the tokens contiguous (slices of a
+    wider row are fine); A, D, dt_bias (nheads,) float32. ``cu_seqlens``,
+    ``state_indices`` and ``has_initial_state`` as :func:`conv_packed_fwd`;
+    ``state`` (slots, nheads, 64, 128) float32 is updated in place (None:
+    every sequence starts from zero and leaves no state). ``max_seqlen``: the
+    longest sequence if the host knows it; it steers the schedule only.
+    Returns y (tokens, nheads, 64); rows of no or of a skipped sequence are not
+    written. ``workspace``: a uint8 CUDA tensor, allocated here when None or too
+    small. With ``check`` the call synchronizes the stream and raises if the
+    kernel reported a failed wait; without it, pass a workspace and call
+    :func:`ssd_check` on it later.
+    """
+    device, code = _cuda(x, 3, "x")
+    dtype = x.dtype
+    tokens, nheads, headdim = shape = x.shape
+    if headdim != SSD_HEADDIM:
+        raise ValueError(f"x must be (tokens, nheads, {SSD_HEADDIM})")
+    cu, nseq = _offsets(cu_seqlens, device)
+    y = x.new_empty(shape) if out is None else out
+    bc = (tokens, B.shape[1], SSD_DSTATE)
+    idx, flags = _slots(nseq, state_indices, has_initial_state, device)
+    slots, st, slot_stride = (0, 0, 0) if state is None else _ssd_state(state, nheads, headdim, SSD_DSTATE, device)
+    args = SSD_PACKED.pack(
+        tokens, nseq, nheads, bc[1], slots, int(max_seqlen), code, 1 if dt_softplus else 0,
+        *_rows("x", x, dtype, shape, device), *_rows("dt", dt, dtype, (tokens, nheads), device),
+        *_rows("B", B, dtype, bc, device), *_rows("C", C, dtype, bc, device), *_rows("z", z, dtype, shape, device),
+        *_rows("out", y, dtype, shape, device), _vector("A", A, nheads, device), _vector("D", D, nheads, device),
+        _vector("dt_bias", dt_bias, nheads, device), st, slot_stride, cu, idx, flags, int(wait_limit_us), 0)
+    need = _workspace_bytes(device, "mamba_ssd_packed_workspace_size", args)
+    workspace, own = _workspace(device, workspace, need)
+    _run(device, stream, _fn("mamba_ssd_packed_fwd", _str, _ptr, _size, _ptr), args, workspace.data_ptr(),
+         workspace.numel())
+    if own:
+        _keep(workspace, stream)
+    if check:
+        ssd_check(workspace, stream)
+    return y
+
+
+def ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, state_indices=None,
+                     out=None, stream=None):
+    """One Mamba-2 decode step for a batch of requests, states in cache slots.
+
+    ``state`` (slots, nheads, headdim, dstate) float32 is updated in place, row
+    b in slot ``state_indices[b]`` (int32; None: slot b); x, z (batch, nheads,
+    headdim), dt (batch, nheads), B, C (batch, ngroups, dstate) all float32 or
+    all bfloat16, the axes behind the batch contiguous; A, D, dt_bias
+    (nheads,) float32. Any headdim, dstate up to 256. Returns y (batch,
+    nheads, headdim); rows whose index lies outside the cache, or is an earlier
+    row's, are skipped (output row and cache stay as they were).
+    """
+    device, code = _cuda(x, 3, "x")
+    dtype = x.dtype
+    batch, nheads, headdim = shape = x.shape
+    if B.dim() != 3:
+        raise ValueError("B must be (batch, ngroups, dstate)")
+    y = x.new_empty(shape) if out is None else out
+    bc = (batch, B.shape[1], B.shape[2])
+    slots, st, slot_stride = _ssd_state(state, nheads, headdim, bc[2], device)
+    args = SSD_UPDATE.pack(
+        batch, nheads, bc[1], headdim, bc[2], slots, code, 1 if dt_softplus else 0, st, slot_stride,
+        *_rows("x", x, dtype, shape, device), *_rows("dt", dt, dtype, (batch, nheads), device),
+        *_rows("B", B, dtype, bc, device), *_rows("C", C, dtype, bc, device), *_rows("z", z, dtype, shape, device),
+        *_rows("out", y, dtype, shape, device), _vector("A", A, nheads, device), _vector("D", D, nheads, device),
+        _vector("dt_bias", dt_bias, nheads, device), _vector("state_indices", state_indices, batch, device, torch.int32))
+    _run(device, stream, _fn("mamba_ssd_state_update", _str, _ptr), args)
+    return y
+
+
+# ---- norm ----------------------------------------------------------------------
+
+def _residual_code(t, dtype):
+    if t.dtype is not dtype and t.dtype is not torch.float32:
+        raise TypeError(f"the residual must be {dtype} or torch.float32, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def norm_fwd(x, weight=None, z=None, residual=None, residual_scale=1.0, eps=1e-5, group_size=None, gate_first=True,
+             out=None, residual_out=None, stream=None):
+    """RMS norm of each row's groups of ``group_size`` channels (None: the row).
+
+    v = x, or x * silu(z) with ``z`` and ``gate_first``; with ``residual``
+    v = residual + residual_scale * v, which is also returned (in residual's
+    dtype, x's or float32); y = v / sqrt(mean(v^2) + eps) * weight, times
+    silu(z) when the gate comes last. x, z (rows, dim) float32 or bfloat16,
+    rows of any stride; weight (dim,) float32 or None. Returns ``(y,
+    residual_out)``, residual_out None without a residual.
+    """
+    device, code = _cuda(x, 2, "x")
+    dtype = x.dtype
+    rows, dim = shape = x.shape
+    y = x.new_empty(shape) if out is None else out
+    res_code, res, ro = code, (0, 0), (0, 0)
+    if residual is not None:
+        res_code = _residual_code(residual, dtype)
+        if residual_out is None:
+            residual_out = residual.new_empty(shape)
+        res = _rows("residual", residual, residual.dtype, shape, device)
+        ro = _rows("residual_out", residual_out, residual.dtype, shape, device)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    args = NORM.pack(rows, dim, dim if group_size is None else group_size, code, res_code, eps, residual_scale,
+                     1 if gate_first else 0, 0, *_rows("x", x, dtype, shape, device),
+                     *_rows("z", z, dtype, shape, device), *res, *ro, *_rows("out", y, dtype, shape, device),
+                     _vector("weight", weight, dim, device))
+    _run(device, stream, _fn("mamba_norm_fwd", _str, _ptr), args)
+    return y, residual_out
+
+
+def norm_bwd(dy, x, weight=None, z=None, residual_out=None, dresidual_out=None, residual_scale=1.0, eps=1e-5,
+             group_size=None, gate_first=True, workspace=None, stream=None):
+    """Gradients of :func:`norm_fwd` for the loss sum(y * dy) + sum(residual_out * dresidual_out).
+
+    ``residual_out`` is the sum that the forward returned (None: it had no
+    residual); ``dresidual_out``, in its dtype, may be None. Returns a dict:
+    dx, dz (None without z) in x's dtype, dresidual (None without a residual)
+    in the residual's, dweight (dim,) float32 (None without weight).
+    ``workspace``: optional uint8 CUDA tensor, allocated here when needed.
+    """
+    device, code = _cuda(x, 2, "x")
+    dtype = x.dtype
+    rows, dim = shape = x.shape
+    out = {"dx": x.new_empty(shape), "dz": None, "dresidual": None, "dweight": None}
+    res_code, ro, dro, dres, dz = code, (0, 0), (0, 0), (0, 0), (0, 0)
+    if residual_out is not None:
+        res_code = _residual_code(residual_out, dtype)
+        ro = _rows("residual_out", residual_out, residual_out.dtype, shape, device)
+        dro = _rows("dresidual_out", dresidual_out, residual_out.dtype, shape, device)
+        out["dresidual"] = residual_out.new_empty(shape)
+        dres = out["dresidual"].data_ptr(), dim
+    elif dresidual_out is not None:
+        raise ValueError("dresidual_out needs residual_out")
+    if z is not None:
+        out["dz"] = x.new_empty(shape)
+        dz = out["dz"].data_ptr(), dim
+    dw = 0
+    if weight is not None:
+        out["dweight"] = torch.empty(dim, dtype=torch.float32, device=device)
+        dw = out["dweight"].data_ptr()
+    args = NORM.pack(rows, dim, dim if group_size is None else group_size, code, res_code, eps, residual_scale,
+                     1 if gate_first else 0, 0, *_rows("x", x, dtype, shape, device),
+                     *_rows("z", z, dtype, shape, device), 0, 0, *ro, 0, 0, _vector("weight", weight, dim, device))
+    grads = NORM_BWD.pack(*_rows("dy", dy, dtype, shape, device), *dro, out["dx"].data_ptr(), dim, *dz, *dres, dw)
+    ws, own = None, False
+    if dw:
+        need = _workspace_bytes(device, "mamba_norm_bwd_workspace_size", args)
+        if need:
+            ws, own = _workspace(device, workspace, need)
+    _run(device, stream, _fn("mamba_norm_bwd", _str, _str, _ptr, _size, _ptr), args, grads,
+         0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
+    if own:
+        _keep(ws, stream)
+    return out
