@@ -211,7 +211,8 @@ struct ConvPackedParams {
     const uint8_t *has_init;
     const float *weight, *bias;
     int width, silu;
-    int64_t tile;             // rows per tile block (set by the launch)
+    int64_t tile, tiles;      // rows per tile, tiles (set by the launch)
+    int w_vec;                // the filters can be read 16 bytes at a time (set by the launch)
 };
 cudaError_t launch_conv_packed(const ConvPackedParams &p, int in_dtype, int num_sms, cudaStream_t stream);
 

@@ -14,6 +14,8 @@
 // backward a team stays on one group of channels and walks down the rows of
 // its slab, so that its share of dw stays in registers; the slabs' shares are
 // added by a second kernel.
+#include <type_traits>
+
 #include "launch.h"
 #include "vec.cuh"
 
@@ -22,6 +24,7 @@ namespace {
 
 constexpr int kWarps = 4;                // warps per block of the warp-team kernels
 constexpr int kMaxBlock = 512;           // threads of a block team
+constexpr int kBwdThreads = 512;         // threads of the backward that run together on an SM
 
 // Sum over a team: `ts` lanes of a warp (a power of two), or the whole block.
 template <bool BLOCK, int K>
@@ -45,10 +48,64 @@ __device__ __forceinline__ void team_sum(float (&v)[K], int ts, float *smem) {
     }
 }
 
+// What the call combines, known at compile time for the usual calls (their
+// kernels then have no branches per vector); kAny looks at the arguments.
+enum Mode { kPlain, kGateFirst, kGateLast, kResidual, kAny };
+
+template <int MODE>
+struct Has {
+    static __device__ __forceinline__ bool z(const NormParams &p) {
+        return MODE == kAny ? p.z != nullptr : MODE == kGateFirst || MODE == kGateLast;
+    }
+    static __device__ __forceinline__ bool first(const NormParams &p) {
+        return MODE == kAny ? p.gate_first != 0 : MODE == kGateFirst;
+    }
+    // residual_out is given exactly when there is a residual
+    static __device__ __forceinline__ bool res(const NormParams &p) {
+        return MODE == kAny ? p.ro != nullptr : MODE == kResidual;
+    }
+};
+
+inline Mode mode_of(const NormParams &p) {
+    if (p.ro) return p.z ? kAny : kResidual;
+    return !p.z ? kPlain : p.gate_first ? kGateFirst : kGateLast;
+}
+
+// f[e] silu(z[e]) in place.
+template <int VEC>
+__device__ __forceinline__ void silu_times(float (&f)[VEC], const float (&z)[VEC]) {
+    if constexpr (VEC == 1) {
+        f[0] *= z[0] * sigmoid(z[0]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const float2 zz = f2(z[e], z[e + 1]);
+            const float2 t = mul2(f2(f[e], f[e + 1]), mul2(zz, sigmoid2(zz)));
+            f[e] = t.x;
+            f[e + 1] = t.y;
+        }
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void sigmoids(const float (&z)[VEC], float (&g)[VEC]) {
+    if constexpr (VEC == 1) {
+        g[0] = sigmoid(z[0]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const float2 t = sigmoid2(f2(z[e], z[e + 1]));
+            g[e] = t.x;
+            g[e + 1] = t.y;
+        }
+    }
+}
+
 // The value that is normed, of VEC channels at element i of the row; `sum` is
 // what residual_out stores.
-template <typename T, typename R, int VEC>
+template <typename T, typename R, int VEC, int MODE>
 struct FwdRow {
+    using H = Has<MODE>;
     const T *x, *z;
     const R *res;
     R *ro;
@@ -56,23 +113,22 @@ struct FwdRow {
     const float *w;
     __device__ __forceinline__ FwdRow(const NormParams &p, int64_t row, int64_t c0)
         : x(static_cast<const T *>(p.x) + row * p.x_sr + c0),
-          z(p.z ? static_cast<const T *>(p.z) + row * p.z_sr + c0 : nullptr),
-          res(p.res ? static_cast<const R *>(p.res) + row * p.res_sr + c0 : nullptr),
-          ro(p.res ? static_cast<R *>(p.ro) + row * p.ro_sr + c0 : nullptr),
+          z(H::z(p) ? static_cast<const T *>(p.z) + row * p.z_sr + c0 : nullptr),
+          res(H::res(p) ? static_cast<const R *>(p.res) + row * p.res_sr + c0 : nullptr),
+          ro(H::res(p) ? static_cast<R *>(p.ro) + row * p.ro_sr + c0 : nullptr),
           y(static_cast<T *>(p.y) + row * p.y_sr + c0), w(p.w ? p.w + c0 : nullptr) {}
 };
 
-template <typename T, typename R, int VEC>
+template <typename T, typename R, int VEC, int MODE>
 __device__ __forceinline__ void norm_value(const NormParams &p, const Raw<T, VEC> &xr, const Raw<T, VEC> &zr,
                                            const Raw<R, VEC> &rr, float (&v)[VEC]) {
     widen<T, VEC>(xr, v);
-    if (p.z && p.gate_first) {
+    if (Has<MODE>::z(p) && Has<MODE>::first(p)) {
         float z[VEC];
         widen<T, VEC>(zr, z);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] *= z[e] * sigmoid(z[e]);
+        silu_times<VEC>(v, z);
     }
-    if (p.res) {
+    if (Has<MODE>::res(p)) {
         float r[VEC];
         widen<R, VEC>(rr, r);
 #pragma unroll
@@ -80,24 +136,23 @@ __device__ __forceinline__ void norm_value(const NormParams &p, const Raw<T, VEC
     }
 }
 
-template <typename T, typename R, int VEC>
-__device__ __forceinline__ void norm_store(const NormParams &p, const FwdRow<T, R, VEC> &row, int64_t i, float r,
+template <typename T, typename R, int VEC, int MODE>
+__device__ __forceinline__ void norm_store(const NormParams &p, const FwdRow<T, R, VEC, MODE> &row, int64_t i, float r,
                                            const float (&v)[VEC], const Raw<T, VEC> &zr) {
     float w[VEC], o[VEC];
     if (row.w) load_f32<VEC>(row.w + i, w);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) o[e] = row.w ? v[e] * r * w[e] : v[e] * r;
-    if (p.z && !p.gate_first) {
+    if (Has<MODE>::z(p) && !Has<MODE>::first(p)) {
         float z[VEC];
         widen<T, VEC>(zr, z);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] *= z[e] * sigmoid(z[e]);
+        silu_times<VEC>(o, z);
     }
     store_raw<T, VEC>(row.y + i, narrow<T, VEC>(o));
 }
 
 // One (row, group) per team; NV vectors per thread in registers.
-template <typename T, typename R, int VEC, int NV, bool BLOCK>
+template <typename T, typename R, int VEC, int NV, bool BLOCK, int MODE>
 __global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarps * 32) norm_fwd_kernel(const NormParams p) {
     __shared__ float smem[32];
     const int ts = BLOCK ? (int)blockDim.x : p.team;
@@ -106,7 +161,7 @@ __global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarps * 32) norm_fwd_kern
                                : static_cast<int64_t>(blockIdx.x) * (blockDim.x / ts) + threadIdx.x / ts;
     const bool on = item < p.rows * p.groups;   // (false only in the last block of warp teams)
     const int64_t row = on ? item / p.groups : 0, c0 = on ? (item % p.groups) * p.gs : 0;
-    const FwdRow<T, R, VEC> q(p, row, c0);
+    const FwdRow<T, R, VEC, MODE> q(p, row, c0);
     const int nvec = on ? static_cast<int>(p.gs / VEC) : 0;
     Raw<T, VEC> xr[NV], zr[NV];
     Raw<R, VEC> rr[NV];
@@ -118,17 +173,17 @@ __global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarps * 32) norm_fwd_kern
         rr[i] = {};
         if (j < nvec) {
             xr[i] = load_raw<T, VEC>(q.x + j * VEC);
-            if (q.z) zr[i] = load_raw<T, VEC>(q.z + j * VEC);
-            if (q.res) rr[i] = load_raw<R, VEC>(q.res + j * VEC);
+            if (Has<MODE>::z(p)) zr[i] = load_raw<T, VEC>(q.z + j * VEC);
+            if (Has<MODE>::res(p)) rr[i] = load_raw<R, VEC>(q.res + j * VEC);
         }
     }
     float v[NV][VEC], ss[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        norm_value<T, R, VEC>(p, xr[i], zr[i], rr[i], v[i]);
+        norm_value<T, R, VEC, MODE>(p, xr[i], zr[i], rr[i], v[i]);
         const int j = lane + i * ts;
         if (j < nvec) {
-            if (q.ro) store_raw<R, VEC>(q.ro + j * VEC, narrow<R, VEC>(v[i]));
+            if (Has<MODE>::res(p)) store_raw<R, VEC>(q.ro + j * VEC, narrow<R, VEC>(v[i]));
 #pragma unroll
             for (int e = 0; e < VEC; ++e) ss[0] = fmaf(v[i][e], v[i][e], ss[0]);
         }
@@ -138,7 +193,7 @@ __global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarps * 32) norm_fwd_kern
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int j = lane + i * ts;
-        if (j < nvec) norm_store<T, R, VEC>(p, q, j * VEC, r, v[i], zr[i]);
+        if (j < nvec) norm_store<T, R, VEC, MODE>(p, q, j * VEC, r, v[i], zr[i]);
     }
 }
 
@@ -147,7 +202,7 @@ template <typename T, typename R, int VEC>
 __global__ void __launch_bounds__(kMaxBlock) norm_fwd_long_kernel(const NormParams p) {
     __shared__ float smem[32];
     const int64_t row = blockIdx.x / p.groups, c0 = (blockIdx.x % p.groups) * p.gs;
-    const FwdRow<T, R, VEC> q(p, row, c0);
+    const FwdRow<T, R, VEC, kAny> q(p, row, c0);
     const int64_t nvec = p.gs / VEC;
     float ss[1] = {0.f};
     auto value = [&](int64_t j, Raw<T, VEC> &zr, float(&v)[VEC]) {
@@ -155,7 +210,7 @@ __global__ void __launch_bounds__(kMaxBlock) norm_fwd_long_kernel(const NormPara
         zr = {};
         if (q.z) zr = load_raw<T, VEC>(q.z + j * VEC);
         if (q.res) rr = load_raw<R, VEC>(q.res + j * VEC);
-        norm_value<T, R, VEC>(p, load_raw<T, VEC>(q.x + j * VEC), zr, rr, v);
+        norm_value<T, R, VEC, kAny>(p, load_raw<T, VEC>(q.x + j * VEC), zr, rr, v);
     };
     for (int64_t j = threadIdx.x; j < nvec; j += blockDim.x) {
         Raw<T, VEC> zr;
@@ -171,64 +226,62 @@ __global__ void __launch_bounds__(kMaxBlock) norm_fwd_long_kernel(const NormPara
         Raw<T, VEC> zr;
         float v[VEC];
         value(j, zr, v);
-        norm_store<T, R, VEC>(p, q, j * VEC, r, v, zr);
+        norm_store<T, R, VEC, kAny>(p, q, j * VEC, r, v, zr);
     }
 }
 
 // ---- backward ----------------------------------------------------------------
 
-template <typename T, typename R, int VEC>
+template <typename T, typename R, int VEC, int MODE>
 struct BwdRow {
+    using H = Has<MODE>;
     const T *dy, *x, *z;
     const R *sum, *ds;
     T *dx, *dz;
     R *dres;
     __device__ __forceinline__ BwdRow(const NormParams &p, const NormBwdParams &g, int64_t row, int64_t c0)
         : dy(static_cast<const T *>(g.dy) + row * g.dy_sr + c0),
-          x(g.need_x ? static_cast<const T *>(p.x) + row * p.x_sr + c0 : nullptr),
-          z(p.z ? static_cast<const T *>(p.z) + row * p.z_sr + c0 : nullptr),
-          sum(p.ro ? static_cast<const R *>(p.ro) + row * p.ro_sr + c0 : nullptr),
-          ds(g.dro ? static_cast<const R *>(g.dro) + row * g.dro_sr + c0 : nullptr),
+          x(!H::res(p) || (H::z(p) && H::first(p)) ? static_cast<const T *>(p.x) + row * p.x_sr + c0 : nullptr),
+          z(H::z(p) ? static_cast<const T *>(p.z) + row * p.z_sr + c0 : nullptr),
+          sum(H::res(p) ? static_cast<const R *>(p.ro) + row * p.ro_sr + c0 : nullptr),
+          ds(H::res(p) && g.dro ? static_cast<const R *>(g.dro) + row * g.dro_sr + c0 : nullptr),
           dx(static_cast<T *>(g.dx) + row * g.dx_sr + c0),
-          dz(p.z ? static_cast<T *>(g.dz) + row * g.dz_sr + c0 : nullptr),
-          dres(p.ro ? static_cast<R *>(g.dres) + row * g.dres_sr + c0 : nullptr) {}
+          dz(H::z(p) ? static_cast<T *>(g.dz) + row * g.dz_sr + c0 : nullptr),
+          dres(H::res(p) ? static_cast<R *>(g.dres) + row * g.dres_sr + c0 : nullptr) {}
 };
 
 // What one thread knows of VEC channels of a row before the reductions.
-template <typename T, typename R, int VEC>
+template <typename T, typename R, int VEC, int MODE>
 struct BwdVec {
+    using H = Has<MODE>;
     Raw<T, VEC> dy, x, z;
     Raw<R, VEC> sum, ds;
-    __device__ __forceinline__ void load(const BwdRow<T, R, VEC> &q, int64_t i) {
+    __device__ __forceinline__ void load(const NormParams &p, const BwdRow<T, R, VEC, MODE> &q, int64_t i) {
         dy = load_raw<T, VEC>(q.dy + i);
-        if (q.x) x = load_raw<T, VEC>(q.x + i);
-        if (q.z) z = load_raw<T, VEC>(q.z + i);
-        if (q.sum) sum = load_raw<R, VEC>(q.sum + i);
-        if (q.ds) ds = load_raw<R, VEC>(q.ds + i);
+        if (!H::res(p) || (H::z(p) && H::first(p))) x = load_raw<T, VEC>(q.x + i);
+        if (H::z(p)) z = load_raw<T, VEC>(q.z + i);
+        if (H::res(p)) sum = load_raw<R, VEC>(q.sum + i);
+        if (H::res(p) && q.ds) ds = load_raw<R, VEC>(q.ds + i);
     }
     // v, and dy as it reaches the norm's output (before the weight)
     __device__ __forceinline__ void values(const NormParams &p, float (&v)[VEC], float (&d)[VEC]) const {
         widen<T, VEC>(dy, d);
-        if (p.ro) widen<R, VEC>(sum, v);
+        if (H::res(p)) widen<R, VEC>(sum, v);
         else widen<T, VEC>(x, v);
-        if (p.z && (!p.ro || !p.gate_first)) {
+        if (H::z(p) && (!H::res(p) || !H::first(p))) {
             float zf[VEC];
             widen<T, VEC>(z, zf);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float s = zf[e] * sigmoid(zf[e]);
-                if (p.gate_first) v[e] *= s;
-                else d[e] *= s;
-            }
+            if (H::first(p)) silu_times<VEC>(v, zf);
+            else silu_times<VEC>(d, zf);
         }
     }
     // the gradients, from r and m = mean(u v) r^3 (u = d w)
-    __device__ __forceinline__ void store(const NormParams &p, const BwdRow<T, R, VEC> &q, int64_t i, float r, float m,
+    __device__ __forceinline__ void store(const NormParams &p, const BwdRow<T, R, VEC, MODE> &q, int64_t i, float r, float m,
                                           const float (&v)[VEC], const float (&d)[VEC], const float (&w)[VEC]) const {
         float dv[VEC], zf[VEC], sg[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) dv[e] = fmaf(r, d[e] * w[e], -m * v[e]);
-        if (q.sum) {
+        if (H::res(p)) {
             if (q.ds) {
                 float t[VEC];
                 widen<R, VEC>(ds, t);
@@ -239,17 +292,17 @@ struct BwdVec {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) dv[e] *= p.scale;
         }
-        if (q.z) {
+        if (H::z(p)) {
             float dz[VEC], f[VEC];
             widen<T, VEC>(z, zf);
-            if (p.gate_first) widen<T, VEC>(x, f);
+            if (H::first(p)) widen<T, VEC>(x, f);
             else widen<T, VEC>(dy, f);
+            sigmoids<VEC>(zf, sg);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                sg[e] = sigmoid(zf[e]);
                 const float slope = sg[e] * fmaf(zf[e], 1.f - sg[e], 1.f);
-                dz[e] = (p.gate_first ? dv[e] : v[e] * r * w[e]) * f[e] * slope;
-                if (p.gate_first) dv[e] *= zf[e] * sg[e];
+                dz[e] = (H::first(p) ? dv[e] : v[e] * r * w[e]) * f[e] * slope;
+                if (H::first(p)) dv[e] *= zf[e] * sg[e];
             }
             store_raw<T, VEC>(q.dz + i, narrow<T, VEC>(dz));
         }
@@ -258,9 +311,9 @@ struct BwdVec {
 };
 
 // Block (slab, group): teams walk rows slab * teams + team, + slabs * teams, ...
-template <typename T, typename R, int VEC, int NV, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarps * 32) norm_bwd_kernel(const NormParams p,
-                                                                                   const NormBwdParams g) {
+template <typename T, typename R, int VEC, int NV, bool BLOCK, int MODE>
+__global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarps * 32, BLOCK ? 1 : kBwdThreads / (kWarps * 32))
+    norm_bwd_kernel(const NormParams p, const NormBwdParams g) {
     extern __shared__ float dwsum[];   // warp teams: the group's share of dw
     __shared__ float smem[64];
     const int ts = BLOCK ? (int)blockDim.x : p.team;
@@ -268,32 +321,34 @@ __global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarps * 32) norm_bwd_kern
     const int lane = threadIdx.x - team * ts;
     const int64_t slab = blockIdx.x / p.groups, c0 = (blockIdx.x % p.groups) * p.gs;
     const int nvec = static_cast<int>(p.gs / VEC);
-    float dw[NV][VEC] = {};
+    float dw[NV][VEC] = {}, w[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) w[i][e] = 1.f;
+        if (p.w && lane + i * ts < nvec) load_f32<VEC>(p.w + c0 + (lane + i * ts) * VEC, w[i]);
+    }
     // every team of a block makes the same number of rounds (the last ones on row 0, without effect)
     for (int64_t r0 = slab * teams; r0 < p.rows; r0 += g.slabs * teams) {
         const int64_t row = r0 + team;
         const bool on = row < p.rows;
-        const BwdRow<T, R, VEC> q(p, g, on ? row : 0, c0);
-        BwdVec<T, R, VEC> in[NV];
+        const BwdRow<T, R, VEC, MODE> q(p, g, on ? row : 0, c0);
+        BwdVec<T, R, VEC, MODE> in[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = lane + i * ts;
             in[i] = {};
-            if (on && j < nvec) in[i].load(q, j * VEC);
+            if (on && j < nvec) in[i].load(p, q, j * VEC);
         }
-        float v[NV][VEC], d[NV][VEC], s[2] = {0.f, 0.f};
+        float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int j = lane + i * ts;
-            in[i].values(p, v[i], d[i]);
-            float w[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) w[e] = 1.f;
-            if (p.w && j < nvec) load_f32<VEC>(p.w + c0 + j * VEC, w);
+            float v[VEC], d[VEC];
+            in[i].values(p, v, d);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                s[0] = fmaf(v[i][e], v[i][e], s[0]);
-                s[1] = fmaf(d[i][e] * w[e], v[i][e], s[1]);
+                s[0] = fmaf(v[e], v[e], s[0]);
+                s[1] = fmaf(d[e] * w[i][e], v[e], s[1]);
             }
         }
         team_sum<BLOCK, 2>(s, ts, smem);
@@ -303,13 +358,11 @@ __global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarps * 32) norm_bwd_kern
         for (int i = 0; i < NV; ++i) {
             const int j = lane + i * ts;
             if (on && j < nvec) {
-                float w[VEC];
+                float v[VEC], d[VEC];
+                in[i].values(p, v, d);
+                in[i].store(p, q, j * VEC, r, m, v, d, w[i]);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) w[e] = 1.f;
-                if (p.w) load_f32<VEC>(p.w + c0 + j * VEC, w);
-                in[i].store(p, q, j * VEC, r, m, v[i], d[i], w);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) dw[i][e] = fmaf(d[i][e], v[i][e] * r, dw[i][e]);
+                for (int e = 0; e < VEC; ++e) dw[i][e] = fmaf(d[e], v[e] * r, dw[i][e]);
             }
         }
     }
@@ -362,12 +415,12 @@ __global__ void __launch_bounds__(kMaxBlock) norm_bwd_long_kernel(const NormPara
     };
     bool first = true;
     for (int64_t row = slab; row < p.rows; row += g.slabs, first = false) {
-        const BwdRow<T, R, VEC> q(p, g, row, c0);
+        const BwdRow<T, R, VEC, kAny> q(p, g, row, c0);
         float s[2] = {0.f, 0.f};
         for (int64_t j = threadIdx.x; j < nvec; j += blockDim.x) {
-            BwdVec<T, R, VEC> in{};
+            BwdVec<T, R, VEC, kAny> in{};
             float v[VEC], d[VEC], w[VEC];
-            in.load(q, j * VEC);
+            in.load(p, q, j * VEC);
             in.values(p, v, d);
             weight(j, w);
 #pragma unroll
@@ -380,9 +433,9 @@ __global__ void __launch_bounds__(kMaxBlock) norm_bwd_long_kernel(const NormPara
         const float r = rsqrtf(s[0] * p.inv_gs + p.eps);
         const float m = s[1] * p.inv_gs * r * r * r;
         for (int64_t j = threadIdx.x; j < nvec; j += blockDim.x) {
-            BwdVec<T, R, VEC> in{};
+            BwdVec<T, R, VEC, kAny> in{};
             float v[VEC], d[VEC], w[VEC];
-            in.load(q, j * VEC);
+            in.load(p, q, j * VEC);
             in.values(p, v, d);
             weight(j, w);
             in.store(p, q, j * VEC, r, m, v, d, w);
@@ -394,20 +447,25 @@ __global__ void __launch_bounds__(kMaxBlock) norm_bwd_long_kernel(const NormPara
     }
 }
 
-// dw[c] = sum over slabs of partial[slab][c], in slab order within 16 strided
-// sums that are then added in order.
-__global__ void __launch_bounds__(512) norm_dw_kernel(const float *partial, float *dw, int64_t slabs, int64_t dim) {
-    __shared__ float acc[16][33];
-    const int cx = threadIdx.x & 31, k = threadIdx.x >> 5;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + cx;
+// dw[c] = sum over slabs of partial[slab][c], in a fixed order: 8 columns per
+// block (32 bytes of a row), 128 strided sums each, those by shuffles and warps.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float *partial, float *dw, int64_t slabs, int64_t dim) {
+    __shared__ float acc[32][8];
+    const int cx = threadIdx.x & 7, k = threadIdx.x >> 3;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + cx;
     float s = 0.f;
-    if (c < dim)
-        for (int64_t i = k; i < slabs; i += 16) s += partial[i * dim + c];
-    acc[k][cx] = s;
+    if (c < dim) {
+#pragma unroll 4
+        for (int64_t i = k; i < slabs; i += 128) s += __ldg(partial + i * dim + c);
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if ((threadIdx.x & 31) < 8) acc[threadIdx.x >> 5][cx] = s;
     __syncthreads();
-    if (k == 0 && c < dim) {
+    if (threadIdx.x < 8 && c < dim) {
+        s = 0.f;
 #pragma unroll
-        for (int i = 1; i < 16; ++i) s += acc[i][cx];
+        for (int i = 0; i < 32; ++i) s += acc[i][cx];
         dw[c] = s;
     }
 }
@@ -419,65 +477,105 @@ struct Teams {
     int ts, nv;
 };
 
-Teams teams_of(int64_t nvec) {
-    if (nvec <= 32 * 4) {
+// nvec vectors of vec elements: sixteen elements per thread, up to thirty-two for
+// the longest rows. (The backward with 8 per thread, twice the threads on a row:
+// 176 us against 135 us for 16384 x 8 groups of 512.)
+Teams teams_of(int64_t nvec, int vec) {
+    const int full = 16 / vec < 8 ? 16 / vec : 8;   // vectors per thread
+    if (nvec <= 32 * full) {
         int ts = 1;
         while (ts < 32 && ts < nvec) ts *= 2;
-        const int64_t n = (nvec + ts - 1) / ts;
-        return {false, ts, n <= 1 ? 1 : n <= 2 ? 2 : 4};
+        int nv = 1;
+        while (static_cast<int64_t>(nv) * ts < nvec) nv *= 2;
+        return {false, ts, nv};
     }
-    // a block: one vector per thread up to 256 threads, then two, then up to four
-    const int nv = nvec <= 256 ? 1 : nvec <= 2 * kMaxBlock ? 2 : 4;
-    if (nvec > nv * kMaxBlock) return {true, kMaxBlock, 0};
-    const int64_t t = (nvec + nv - 1) / nv;
-    return {true, static_cast<int>((t + 31) / 32 * 32), nv};
+    for (int nv = full; nv <= 8 && nv * vec <= 32; nv *= 2)
+        if (nvec <= static_cast<int64_t>(nv) * kMaxBlock) {
+            const int64_t t = (nvec + nv - 1) / nv;
+            return {true, static_cast<int>((t + 31) / 32 * 32), nv};
+        }
+    return {true, kMaxBlock, 0};
+}
+
+// f(NV) with the plan's vectors per thread as a compile-time value (those that
+// a vector width can have: up to twice 16 elements, at most 8 vectors).
+template <int VEC, typename F>
+cudaError_t with_nv(int nv, F f) {
+    constexpr int kMost = 32 / VEC < 8 ? 32 / VEC : 8;
+    if constexpr (kMost >= 8)
+        if (nv == 8) return f(std::integral_constant<int, 8>());
+    if constexpr (kMost >= 4)
+        if (nv == 4) return f(std::integral_constant<int, 4>());
+    if (nv == 2) return f(std::integral_constant<int, 2>());
+    return f(std::integral_constant<int, 1>());
+}
+
+// f(MODE) with the call's mode as a compile-time value: the usual ones for the
+// vectors of 8 bytes and more, kAny for everything else.
+template <typename T, typename R, int VEC, typename F>
+cudaError_t with_mode(const NormParams &p, F f) {
+    if constexpr (VEC * sizeof(T) >= 8) {
+        const Mode m = mode_of(p);
+        if (m == kResidual) return f(std::integral_constant<int, kResidual>());
+        if constexpr (std::is_same<T, R>::value) {   // (without a residual R is T)
+            if (m == kPlain) return f(std::integral_constant<int, kPlain>());
+            if (m == kGateFirst) return f(std::integral_constant<int, kGateFirst>());
+            if (m == kGateLast) return f(std::integral_constant<int, kGateLast>());
+        }
+    }
+    return f(std::integral_constant<int, kAny>());
 }
 
 template <typename T, typename R, int VEC>
 cudaError_t fwd_vec(const NormParams &p0, cudaStream_t stream) {
     NormParams p = p0;
-    const Teams t = teams_of(p.gs / VEC);
+    const Teams t = teams_of(p.gs / VEC, VEC);
     const int64_t items = p.rows * p.groups;
     p.team = t.ts;
-    if (!t.block) {
-        const int per = kWarps * 32 / t.ts;
-        const unsigned grid = static_cast<unsigned>((items + per - 1) / per);
-        if (t.nv == 1) norm_fwd_kernel<T, R, VEC, 1, false><<<grid, kWarps * 32, 0, stream>>>(p);
-        else if (t.nv == 2) norm_fwd_kernel<T, R, VEC, 2, false><<<grid, kWarps * 32, 0, stream>>>(p);
-        else norm_fwd_kernel<T, R, VEC, 4, false><<<grid, kWarps * 32, 0, stream>>>(p);
-    } else {
-        const unsigned grid = static_cast<unsigned>(items);
-        if (t.nv == 0) norm_fwd_long_kernel<T, R, VEC><<<grid, t.ts, 0, stream>>>(p);
-        else if (t.nv == 1) norm_fwd_kernel<T, R, VEC, 1, true><<<grid, t.ts, 0, stream>>>(p);
-        else if (t.nv == 2) norm_fwd_kernel<T, R, VEC, 2, true><<<grid, t.ts, 0, stream>>>(p);
-        else norm_fwd_kernel<T, R, VEC, 4, true><<<grid, t.ts, 0, stream>>>(p);
+    if (t.nv == 0) {
+        norm_fwd_long_kernel<T, R, VEC><<<static_cast<unsigned>(items), t.ts, 0, stream>>>(p);
+        return cudaGetLastError();
     }
-    return cudaGetLastError();
+    return with_mode<T, R, VEC>(p, [&](auto mode) {
+        return with_nv<VEC>(t.nv, [&](auto nv) {
+            constexpr int NV = decltype(nv)::value, MODE = decltype(mode)::value;
+            if (t.block) {
+                norm_fwd_kernel<T, R, VEC, NV, true, MODE><<<static_cast<unsigned>(items), t.ts, 0, stream>>>(p);
+            } else {
+                const int per = kWarps * 32 / t.ts;
+                norm_fwd_kernel<T, R, VEC, NV, false, MODE>
+                    <<<static_cast<unsigned>((items + per - 1) / per), kWarps * 32, 0, stream>>>(p);
+            }
+            return cudaGetLastError();
+        });
+    });
 }
 
 template <typename T, typename R, int VEC>
 cudaError_t bwd_vec(const NormParams &p0, const NormBwdParams &g, cudaStream_t stream) {
     NormParams p = p0;
-    const Teams t = teams_of(p.gs / VEC);
+    const Teams t = teams_of(p.gs / VEC, VEC);
     p.team = t.ts;
     const unsigned grid = static_cast<unsigned>(g.slabs * p.groups);
-    const size_t sm = static_cast<size_t>(p.gs) * sizeof(float);
-    if (!t.block) {
-        if (t.nv == 1) norm_bwd_kernel<T, R, VEC, 1, false><<<grid, kWarps * 32, sm, stream>>>(p, g);
-        else if (t.nv == 2) norm_bwd_kernel<T, R, VEC, 2, false><<<grid, kWarps * 32, sm, stream>>>(p, g);
-        else norm_bwd_kernel<T, R, VEC, 4, false><<<grid, kWarps * 32, sm, stream>>>(p, g);
-    } else if (t.nv == 0) {
+    cudaError_t e;
+    if (t.nv == 0) {
         norm_bwd_long_kernel<T, R, VEC><<<grid, t.ts, 0, stream>>>(p, g);
-    } else if (t.nv == 1) {
-        norm_bwd_kernel<T, R, VEC, 1, true><<<grid, t.ts, 0, stream>>>(p, g);
-    } else if (t.nv == 2) {
-        norm_bwd_kernel<T, R, VEC, 2, true><<<grid, t.ts, 0, stream>>>(p, g);
+        e = cudaGetLastError();
     } else {
-        norm_bwd_kernel<T, R, VEC, 4, true><<<grid, t.ts, 0, stream>>>(p, g);
+        e = with_mode<T, R, VEC>(p, [&](auto mode) {
+            return with_nv<VEC>(t.nv, [&](auto nv) {
+                constexpr int NV = decltype(nv)::value, MODE = decltype(mode)::value;
+                if (t.block)
+                    norm_bwd_kernel<T, R, VEC, NV, true, MODE><<<grid, t.ts, 0, stream>>>(p, g);
+                else
+                    norm_bwd_kernel<T, R, VEC, NV, false, MODE>
+                        <<<grid, kWarps * 32, static_cast<size_t>(p.gs) * sizeof(float), stream>>>(p, g);
+                return cudaGetLastError();
+            });
+        });
     }
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !g.dw || g.partial == g.dw) return e;
-    norm_dw_kernel<<<static_cast<unsigned>((p.dim + 31) / 32), 512, 0, stream>>>(g.partial, g.dw, g.slabs, p.dim);
+    norm_dw_kernel<<<static_cast<unsigned>((p.dim + 7) / 8), 1024, 0, stream>>>(g.partial, g.dw, g.slabs, p.dim);
     return cudaGetLastError();
 }
 
@@ -500,9 +598,11 @@ int vector_width(const NormParams &p, const NormBwdParams *g, int eb, int rb) {
 }  // namespace
 
 int64_t norm_bwd_slabs(int64_t rows, int64_t dim, int64_t gs, int num_sms) {
-    // about 16 warps per SM over all groups, at least 4 rows per slab
+    // As many blocks as run together (512 threads of 128 registers per SM; twice as
+    // many blocks, in two rounds: 143 us against 135 us), at least 4 rows per slab.
     const int64_t groups = dim / gs;
-    const int64_t blocks = static_cast<int64_t>(num_sms) * (gs <= 1024 ? 8 : 3);
+    const int64_t threads = gs <= 512 ? kWarps * 32 : min64((gs + 511) / 512 * 32, kMaxBlock);
+    const int64_t blocks = num_sms * (kBwdThreads / threads);
     const int64_t want = (blocks + groups - 1) / groups;
     const int64_t most = (rows + 3) / 4;
     return max64(1, min64(want, most));

@@ -92,6 +92,16 @@ inline bool vec_ok(const void *ptr, int64_t stride, int eb, int vec) {
 // sigmoid(z) = 1 / (1 + e^-z); e^-z = inf gives 0.
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
+// sigmoid of a pair, 1 / (1 + e^-z), to a few float32 roundings (e^-z = inf gives 0).
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+    const float2 e = ex2x2(mul2(z, f2(-kLog2e, -kLog2e)));
+    const float2 s = add2(e, f2(1.f, 1.f));
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(s.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(s.y));
+    return r;
+}
+
 // softplus close to float32 rounding (log1p(e) = e p(e), p of degree 9 by
 // fit_log1p.py 9: 1.6e-7 relative), for steps that enter float32 states.
 __device__ __forceinline__ float softplus_fine(float v) {
