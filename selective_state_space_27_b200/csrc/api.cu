@@ -849,11 +849,11 @@ static ms_status check_ssd_packed(const ms_ssd_packed_args *a) {
     if (a->tokens < 0 || a->tokens > kMaxRows - 64 * 1024 || a->max_seqlen < 0)
         return invalid("tokens must be in [0, 2^31 - 2^16) and max_seqlen not negative");
     if (a->nheads > 65535) return unsupported("nheads above 65535");
-    if (a->nseq < 0 || a->nseq > (int64_t(1) << 27) || a->nseq * a->nheads > (int64_t(1) << 27) ||
-        (a->tokens / 256 + a->nseq) * a->nheads > kMaxRows)
-        return unsupported("too many sequences or segments times heads for one launch");
     const ms_status st = check_slots(a->nseq, a->slots, a->state, a->state_indices, a->has_initial_state, true);
     if (st != MS_OK) return st;
+    if (a->nseq > (int64_t(1) << 27) || a->nseq * a->nheads > (int64_t(1) << 27) ||
+        (a->tokens / 256 + a->nseq) * a->nheads > kMaxRows)
+        return unsupported("too many sequences or segments times heads for one launch");
     if (a->nseq == 0) return MS_OK;
     if (!a->cu_seqlens || !a->A) return invalid("cu_seqlens and A are required");
     if (a->tokens > 0 && (!a->x || !a->dt || !a->B || !a->C || !a->y)) return invalid("x, dt, B, C and y are required");

@@ -117,7 +117,15 @@ __device__ __forceinline__ void sequence_start(const ConvPackedParams &p, const 
             store_raw<T, VEC>(y + (q.begin + static_cast<int64_t>(j)) * p.y_st, f.apply(win));
         }
     }
-    if (W == 1 || !p.state) return;
+    if constexpr (W == 1) {
+        // no history: the tiles take every token, except in the single-token form, which has none
+        if (!p.cu) {
+            widen<T, VEC>(load_raw<T, VEC>(x + q.begin * p.x_st), win[0]);
+            store_raw<T, VEC>(y + q.begin * p.y_st, f.apply(win));
+        }
+        return;
+    }
+    if (!p.state) return;
     // the last W - 1 of (history, inputs)
 #pragma unroll
     for (int j = 0; j + 1 < W; ++j) {

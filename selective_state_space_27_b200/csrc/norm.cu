@@ -216,7 +216,6 @@ __global__ void __launch_bounds__(kMaxBlock) norm_fwd_long_kernel(const NormPara
         Raw<T, VEC> zr;
         float v[VEC];
         value(j, zr, v);
-        if (q.ro) store_raw<R, VEC>(q.ro + j * VEC, narrow<R, VEC>(v));
 #pragma unroll
         for (int e = 0; e < VEC; ++e) ss[0] = fmaf(v[e], v[e], ss[0]);
     }
@@ -226,6 +225,7 @@ __global__ void __launch_bounds__(kMaxBlock) norm_fwd_long_kernel(const NormPara
         Raw<T, VEC> zr;
         float v[VEC];
         value(j, zr, v);
+        if (q.ro) store_raw<R, VEC>(q.ro + j * VEC, narrow<R, VEC>(v));
         norm_store<T, R, VEC, kAny>(p, q, j * VEC, r, v, zr);
     }
 }
