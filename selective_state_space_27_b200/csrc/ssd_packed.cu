@@ -69,7 +69,7 @@ constexpr float kMinStep = -160.f;                // smallest log2 decay of one 
 constexpr uint32_t kAtom = kQ * 128;              // 128 rows of 128 bytes
 constexpr uint32_t kOffX = 0;                     // X: two buffers x two heads x (128 tokens x 64)
 constexpr uint32_t kOffB = 4 * kAtom;             // B: 128 tokens x 128, two atoms
-constexpr uint32_t kOffC = 6 * kAtom;             // C (in the states kernel a second buffer of B)
+constexpr uint32_t kOffC = 6 * kAtom;             // C
 constexpr uint32_t kOffW = 8 * kAtom;             // the hi terms of w X of both heads
 constexpr uint32_t kOffH = 10 * kAtom;            // H of both heads (128 rows n x 64 bf16 along p each), or the lo terms
 constexpr uint32_t kOffStep = 12 * kAtom;         // StepData[kSteps][2 heads]
@@ -104,9 +104,18 @@ constexpr uint32_t kOffBar = kOffStep + kSteps * 2 * sizeof(StepData);
 // for it; and what the issuing warp waits for follows from what it issues later.
 enum Bar { kFull, kXFull0, kXFull1, kGFull, kWReady, kMReady, kSFull, kYFull, kYStore0, kYStore1,
            kHReady, kYFree, kDrain, kStep0, kSFree0 = kStep0 + 2 * kSteps, kNumBars = kSFree0 + kSteps };
-constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;   // tensor memory address, abort flag
-constexpr uint32_t kSmemBytes = kOffMisc + 16;
+constexpr uint32_t kOffTmem = kNumBars * 8;             // behind the barriers: tensor memory address, abort flag
+constexpr uint32_t kSmemBytes = kOffBar + kOffTmem + 16;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+// The states kernel: X once, B and both terms of w X twice (the products of one
+// chunk run while the next one's w X is made).
+constexpr uint32_t kStB = 2 * kAtom, kStW = 6 * kAtom, kStL = 10 * kAtom, kStStep = 14 * kAtom;
+struct alignas(16) StateStep {
+    float w[kQ], decay;   // 2^(s to the segment's end) delta_i; decay from this chunk to the segment's end
+};
+constexpr uint32_t kStBar = kStStep + 4 * sizeof(StateStep);   // StateStep[2 buffers][2 heads]
+constexpr uint32_t kStSmemBytes = kStBar + kOffTmem + 16;
+static_assert(kStSmemBytes <= 232448, "shared memory per CTA");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColG = 0, kColM = 128, kColY = 256, kColS = 384;   // M', Y and S: 64 columns per head
@@ -217,6 +226,35 @@ __device__ __forceinline__ float delta_of(const SsdPackedParams &p, float dt, fl
 }
 
 __device__ __forceinline__ float log2_decay(float delta, float A2) { return fmaxf(delta * A2, kMinStep); }
+
+// Exclusive suffix sums over 128 tokens, four per lane, and the sum of all, of two chunks.
+__device__ __forceinline__ void suffix_sums2(const float (&a)[2][4], int lane, float (&suf)[2][4], float (&all)[2])
+{
+    float dn[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        suf[u][3] = 0.f;
+#pragma unroll
+        for (int k = 2; k >= 0; --k) suf[u][k] = suf[u][k + 1] + a[u][k + 1];
+        dn[u] = suf[u][0] + a[u][0];
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float d0 = __shfl_down_sync(0xffffffffu, dn[0], o), d1 = __shfl_down_sync(0xffffffffu, dn[1], o);
+        if (lane + o < 32) {
+            dn[0] += d0;
+            dn[1] += d1;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        all[u] = __shfl_sync(0xffffffffu, dn[u], 0);
+        float after = __shfl_down_sync(0xffffffffu, dn[u], 1);
+        if (lane == 31) after = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) suf[u][k] += after;
+    }
+}
 
 // Inclusive prefix and exclusive suffix sums over 128 tokens, four per lane.
 __device__ __forceinline__ void token_sums(const float (&a)[4], int lane, float (&pre)[4], float (&suf)[4], float &all)
@@ -330,8 +368,8 @@ __device__ __forceinline__ Pair pair_of(const SsdPackedParams &p, int i)
 
 // Set up by all threads: barriers, tensor memory, the segment; false when the
 // CTA has nothing to do (then nothing is allocated).
-__device__ __forceinline__ bool setup(const SsdPackedParams &p, uint8_t *smem, uint32_t base, int64_t place, int nh,
-                                      Segment &g, int &slot, uint32_t &tmem, bool last_too)
+__device__ __forceinline__ bool setup(const SsdPackedParams &p, uint8_t *smem, uint32_t base, uint32_t off_bar,
+                                      int64_t place, int nh, Segment &g, int &slot, uint32_t &tmem, bool last_too)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (base & 1023u) {
@@ -344,20 +382,20 @@ __device__ __forceinline__ bool setup(const SsdPackedParams &p, uint8_t *smem, u
     slot = p.state || p.idx ? block_slot(p.idx, g.seq, p.slots) : 0;
     if (slot < 0) return false;
     if (threadIdx.x == 0) {
-        auto init = [&](int b, int count) { mbar_init(base + kOffBar + 8u * (uint32_t)b, (uint32_t)count); };
+        auto init = [&](int b, int count) { mbar_init(base + off_bar + 8u * (uint32_t)b, (uint32_t)count); };
         for (int b : {kXFull0, kXFull1, kGFull, kSFull, kYFull, kDrain}) init(b, 1);
         init(kFull, 2);   // B and C
         for (int b : {kWReady, kMReady, kHReady, kYFree, kYStore0, kYStore1}) init(b, 8 * nh);
         for (int i = 0; i < 2 * kSteps; ++i) init(kStep0 + i, 32);
         for (int i = 0; i < kSteps; ++i) init(kSFree0 + i, 1);
-        *reinterpret_cast<volatile int *>(smem + kOffMisc + 8) = 0;
+        *reinterpret_cast<volatile int *>(smem + off_bar + kOffTmem + 8) = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kMmaWarp) tmem_alloc(base + kOffMisc, kTmemCols);
+    if (warp == kMmaWarp) tmem_alloc(base + off_bar + kOffTmem, kTmemCols);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
-    tmem = *reinterpret_cast<volatile uint32_t *>(smem + kOffMisc);
+    tmem = *reinterpret_cast<volatile uint32_t *>(smem + off_bar + kOffTmem);
     return true;
 }
 
@@ -377,7 +415,9 @@ __device__ __forceinline__ void teardown(uint32_t tmem)
 // zero for the others, and its decay. Chunks run from the segment's end to its
 // start: the decay of what follows a chunk is then a sum that ends at the
 // segment's end, the weights count to there and the chunks' products add up
-// without rescaling. X and B have two buffers (xfull: both landed).
+// without rescaling. Its barriers: xfull0 X, gfull / yfull B (by buffer), wready,
+// step (by buffer and head) and sfree (by buffer: the products of the chunk are
+// done) as above; each one's next phase needs what its waiters do next.
 __global__ void __launch_bounds__(kThreads, 1)
 ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap b_map,
                          const SsdPackedParams p)
@@ -391,67 +431,91 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
     Segment g;
     int slot;
     uint32_t tmem;
-    if (!setup(p, smem, base, place, hp.nh, g, slot, tmem, false)) return;
-    auto bar = [&](int i) { return base + kOffBar + 8u * (uint32_t)i; };
-    StepData *step = reinterpret_cast<StepData *>(smem + kOffStep);
+    if (!setup(p, smem, base, kStBar, place, hp.nh, g, slot, tmem, false)) return;
+    auto bar = [&](int i) { return base + kStBar + 8u * (uint32_t)i; };
+    StateStep *step = reinterpret_cast<StateStep *>(smem + kStStep);
     const int K = (g.len + kQ - 1) / kQ;
-    const Waiter wait{base + kOffBar, reinterpret_cast<volatile int *>(smem + kOffMisc + 8), p.status, p.wait_limit_ns};
+    const Waiter wait{base + kStBar, reinterpret_cast<volatile int *>(smem + kStBar + kOffTmem + 8), p.status,
+                      p.wait_limit_ns};
+    auto phase = [](int i) { return (uint32_t)(i >> 1) & 1u; };   // of the barriers with two buffers
+    auto bfull = [](int i) { return i & 1 ? kYFull : kGFull; };
 
     if (warp == kStepWarp || warp == kStepWarp + 1) {
         const int head = warp - kStepWarp, h = hp.h + head;
         if (head < hp.nh) {
             const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
             const uint16_t *dtp = reinterpret_cast<const uint16_t *>(p.dt) + (int64_t)g.row * p.dt_st + h;
-            float dtv[4], after = 0.f;   // the step inputs of the next chunk; decay behind it
-            load_steps(dtp, p.dt_st, (K - 1) * kQ + 4 * lane, g.len, dtv);
-            for (int i = 0; i < K; ++i) {
-                if (i >= kSteps) wait(kSFree0 + step_of(i), step_phase(i - kSteps));
-                float d[4], a[4], pre[4], suf[4], all, w[4];
+            // Two chunks at a time: the sums' shuffles wait for each other, and behind the
+            // products' operand reads; those of two chunks overlap.
+            float dtv[2][4], after = 0.f;   // the step inputs of the next two chunks; decay behind them
+            auto fetch = [&](int i, float (&v)[4]) {
+                if (i < K) load_steps(dtp, p.dt_st, (K - 1 - i) * kQ + 4 * lane, g.len, v);
+            };
+            fetch(0, dtv[0]);
+            fetch(1, dtv[1]);
+            for (int i0 = 0; i0 < K; i0 += 2) {
+                float d[2][4], a[2][4], suf[2][4], all[2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    d[j] = delta_of(p, dtv[j], bias);
-                    a[j] = log2_decay(d[j], A2);
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        d[u][j] = delta_of(p, dtv[u][j], bias);
+                        a[u][j] = log2_decay(d[u][j], A2);
+                    }
+                    fetch(i0 + 2 + u, dtv[u]);
                 }
-                if (i + 1 < K) load_steps(dtp, p.dt_st, (K - 2 - i) * kQ + 4 * lane, g.len, dtv);
-                token_sums(a, lane, pre, suf, all);
+                suffix_sums2(a, lane, suf, all);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = ex2(suf[j] + after) * d[j];
-                after += all;
-                StepData &st = step[2 * step_of(i) + head];
-                *reinterpret_cast<float4 *>(st.w + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
-                if (lane == 0) st.s[0] = after;
-                mbar_arrive(bar(kStep0 + 2 * step_of(i) + head));
+                for (int u = 0; u < 2; ++u) {
+                    const int i = i0 + u;
+                    if (i >= K) break;
+                    float w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = ex2(suf[u][j] + after) * d[u][j];
+                    after += all[u];
+                    if (i >= 2) wait(kSFree0 + (i & 1), phase(i - 2));
+                    StateStep &st = step[2 * (i & 1) + head];
+                    *reinterpret_cast<float4 *>(st.w + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
+                    if (lane == 0) st.decay = after;
+                    mbar_arrive(bar(kStep0 + 2 * (i & 1) + head));
+                }
             }
             if (lane == 0) p.seg_decay[place * p.nheads + h] = after;
         }
     } else if (warp == kTmaWarp) {
-        int issued = 0;
         for (int i = 0; i < K; ++i) {
-            if (i >= 2) wait(kSFree0 + step_of(i - 2), step_phase(i - 2));   // (buffers of chunk i - 2 free)
+            const int row = g.row + (K - 1 - i) * kQ;
+            if (i >= 2) wait(kSFree0 + (i & 1), phase(i - 2));
             if (lane == 0) {
-                const int row = g.row + (K - 1 - i) * kQ, st = i & 1;
-                const uint32_t full = bar(kXFull0 + st), x = base + kOffX + (uint32_t)(2 * st) * kAtom;
-                const uint32_t b = base + kOffB + (uint32_t)(2 * st) * kAtom;
-                mbar_arrive_tx(full, (uint32_t)(2 + hp.nh) * kAtom);
-                for (int j = 0; j < hp.nh; ++j) tma_load_2d(x + (uint32_t)j * kAtom, &x_map, full, (hp.h + j) * kP, row);
+                const uint32_t full = bar(bfull(i)), b = base + kStB + (uint32_t)(2 * (i & 1)) * kAtom;
+                mbar_arrive_tx(full, 2 * kAtom);
                 tma_load_2d(b, &b_map, full, hp.group * kN, row);
                 tma_load_2d(b + kAtom, &b_map, full, hp.group * kN + 64, row);
             }
-            issued = i + 1;
+            if (i > 0) wait(kWReady, (i - 1) & 1);
+            if (lane == 0) {
+                mbar_arrive_tx(bar(kXFull0), (uint32_t)hp.nh * kAtom);
+                for (int j = 0; j < hp.nh; ++j) {
+                    tma_load_2d(base + (uint32_t)j * kAtom, &x_map, bar(kXFull0), (hp.h + j) * kP, row);
+                    if (i + 1 < K) tma_prefetch_2d(&x_map, (hp.h + j) * kP, row - kQ);
+                }
+            }
+            __syncwarp();
         }
-        if (lane == 0)   // loads in flight must land
-            for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait(bar(kXFull0 + (i & 1)), (uint32_t)(i >> 1) & 1u);
+        if (lane == 0) {   // loads in flight must land
+            mbar_wait(bar(kXFull0), (K - 1) & 1);
+            for (int i = max(0, K - 2); i < K; ++i) mbar_wait(bar(bfull(i)), phase(i));
+        }
         __syncwarp();
     } else if (warp == kMmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < K; ++i) {
-                wait.one(kXFull0 + (i & 1), (uint32_t)(i >> 1) & 1u);
+                wait.one(bfull(i), phase(i));
                 wait.one(kWReady, i & 1);
                 tc_after_sync();
-                issue_state_product(tmem, base + kOffB + (uint32_t)(2 * (i & 1)) * kAtom, base + kOffW, base + kOffH,
-                                    i > 0);
-                mma_commit(bar(kSFull));
-                mma_commit(bar(kSFree0 + step_of(i)));
+                const uint32_t two = (uint32_t)(2 * (i & 1)) * kAtom;
+                issue_state_product(tmem, base + kStB + two, base + kStW + two, base + kStL + two, i > 0);
+                mma_commit(bar(kSFree0 + (i & 1)));
             }
             mma_commit(bar(kDrain));   // every MMA must finish before the tensor memory is freed
             mbar_wait(bar(kDrain), 0);
@@ -463,44 +527,40 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
         const bool resumed = g.seg == 0 && p.state && p.has_init && p.has_init[g.seq];
         const float *cache = resumed ? p.state + slot * p.s_slot + (int64_t)h * (kP * kN) : nullptr;
         for (int i = 0; i < K; ++i) {
-            wait(kStep0 + 2 * step_of(i) + head, step_phase(i));
-            wait(kXFull0 + (i & 1), (uint32_t)(i >> 1) & 1u);
-            if (i > 0) wait(kSFull, (i - 1) & 1);
-            {
-                const float w = step[2 * step_of(i) + head].w[r];
-                const uint32_t x = base + kOffX + (uint32_t)(2 * (i & 1) + head) * kAtom;
+            wait(kStep0 + 2 * (i & 1) + head, phase(i));
+            wait(kXFull0, i & 1);
+            if (i >= 2) wait(kSFree0 + (i & 1), phase(i - 2));
+            const float w = step[2 * (i & 1) + head].w[r];
+            const uint32_t tiles = (uint32_t)(2 * (i & 1) + head) * kAtom;
 #pragma unroll
-                for (int q = 4 * hq; q < 4 * hq + 4; ++q) {
-                    const uint32_t at = (uint32_t)head * kAtom + sw128((uint32_t)r, (uint32_t)q);
-                    uint32_t hi[4], lo[4];
-                    split(ld_shared_v4(x + sw128((uint32_t)r, (uint32_t)q)), w, hi, lo);
-                    st_shared_v4(base + kOffW + at, hi[0], hi[1], hi[2], hi[3]);
-                    st_shared_v4(base + kOffH + at, lo[0], lo[1], lo[2], lo[3]);
-                }
+            for (int q = 4 * hq; q < 4 * hq + 4; ++q) {
+                const uint32_t at = sw128((uint32_t)r, (uint32_t)q);
+                uint32_t hi[4], lo[4];
+                split(ld_shared_v4(base + (uint32_t)head * kAtom + at), w, hi, lo);
+                st_shared_v4(base + kStW + tiles + at, hi[0], hi[1], hi[2], hi[3]);
+                st_shared_v4(base + kStL + tiles + at, lo[0], lo[1], lo[2], lo[3]);
             }
             async_proxy_fence();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kWReady));
         }
-        wait(kSFull, (K - 1) & 1);
-        {
-            tc_after_sync();
-            const float f = ex2(step[2 * step_of(K - 1) + head].s[0]);
-            float v[32];
-            if (cache) {
-                // the third kernel's first segment reads the initial state from its copy: its
-                // last segment replaces the one in the cache
-                load_state(cache, r, hq, v);
-                store_state(seg_state(p, g.base + g.nseg - 1, h), r, hq, v);
-                float t[32];
-                tmem_load32(tl + 32u * hq, t);
+        wait(kSFree0 + ((K - 1) & 1), phase(K - 1));
+        tc_after_sync();
+        const float f = ex2(step[2 * ((K - 1) & 1) + head].decay);
+        float v[32];
+        if (cache) {
+            // the third kernel's first segment reads the initial state from its copy: its
+            // last segment replaces the one in the cache
+            load_state(cache, r, hq, v);
+            store_state(seg_state(p, g.base + g.nseg - 1, h), r, hq, v);
+            float t[32];
+            tmem_load32(tl + 32u * hq, t);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = fmaf(f, v[j], t[j]);
-            } else {
-                tmem_load32(tl + 32u * hq, v);
-            }
-            store_state(seg_state(p, place, h), r, hq, v);
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(f, v[j], t[j]);
+        } else {
+            tmem_load32(tl + 32u * hq, v);
         }
+        store_state(seg_state(p, place, h), r, hq, v);
     }
     teardown(tmem);
 }
@@ -523,15 +583,28 @@ __global__ void __launch_bounds__(256) ssd_packed_pass_kernel(const SsdPackedPar
     const int64_t step = p.nheads * (int64_t)(kP * kN / 4);
     float4 *at = reinterpret_cast<float4 *>(seg_state(p, base, h)) + part * 256 + threadIdx.x;
     float4 v = __ldcg(at);
-    for (int m = 1; m + 1 < nseg; ++m) {
-        at += step;
-        const float4 a = __ldcg(at);
-        const float f = ex2(__ldcg(p.seg_decay + (base + m) * p.nheads + h));
-        v.x = fmaf(f, v.x, a.x);
-        v.y = fmaf(f, v.y, a.y);
-        v.z = fmaf(f, v.z, a.z);
-        v.w = fmaf(f, v.w, a.w);
-        __stcg(at, v);
+    constexpr int U = 8;   // segments loaded ahead
+    for (int m = 1; m + 1 < nseg; m += U) {
+        const int n = min(U, nseg - 1 - m);
+        float4 a[U];
+        float f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u < n) {
+                a[u] = __ldcg(at + (u + 1) * step);
+                f[u] = __ldcg(p.seg_decay + (base + m + u) * p.nheads + h);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u < n) {
+                const float e = ex2(f[u]);
+                v.x = fmaf(e, v.x, a[u].x);
+                v.y = fmaf(e, v.y, a[u].y);
+                v.z = fmaf(e, v.z, a[u].z);
+                v.w = fmaf(e, v.w, a[u].w);
+                __stcg(at + (u + 1) * step, v);
+            }
+        at += U * step;
     }
 }
 
@@ -599,11 +672,11 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
     Segment g;
     int slot;
     uint32_t tmem;
-    if (!setup(p, smem, base, place, hp.nh, g, slot, tmem, true)) return;
+    if (!setup(p, smem, base, kOffBar, place, hp.nh, g, slot, tmem, true)) return;
     auto bar = [&](int i) { return base + kOffBar + 8u * (uint32_t)i; };
     StepData *step = reinterpret_cast<StepData *>(smem + kOffStep);
     const int K = (g.len + kQ - 1) / kQ;
-    const Waiter wait{base + kOffBar, reinterpret_cast<volatile int *>(smem + kOffMisc + 8), p.status, p.wait_limit_ns};
+    const Waiter wait{base + kOffBar, reinterpret_cast<volatile int *>(smem + kOffBar + kOffTmem + 8), p.status, p.wait_limit_ns};
 
     if (warp == kStepWarp || warp == kStepWarp + 1) {
         // ---- step data of one head, up to kSteps chunks ahead ----
@@ -1001,13 +1074,13 @@ cudaError_t launch_ssd_packed(const SsdPackedParams &p, cudaStream_t stream)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e == cudaSuccess && p.seg_chunks)
         e = cudaFuncSetAttribute(ssd_packed_states_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)kSmemBytes);
+                                 (int)kStSmemBytes);
     if (e == cudaSuccess) e = cudaMemsetAsync(p.status, 0, sizeof(int), stream);
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(ssd_packed_places(p.tokens, p.nseq, p.seg_chunks) *
                                                 pairs_of(p.nheads, p.ngroups));
     if (p.seg_chunks) {
-        ssd_packed_states_kernel<<<grid, kThreads, kSmemBytes, stream>>>(xm, bm, p);
+        ssd_packed_states_kernel<<<grid, kThreads, kStSmemBytes, stream>>>(xm, bm, p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         ssd_packed_pass_kernel<<<static_cast<unsigned>(p.nseq * p.nheads * (kP * kN / 4 / 256)), 256, 0, stream>>>(p);
