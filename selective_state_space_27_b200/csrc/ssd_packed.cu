@@ -168,46 +168,65 @@ struct Segment {
 // segments of Qs tokens, sequence s starts at place cu[s] / Qs + s: since
 // ceil(len / Qs) <= floor((cu + len) / Qs) - floor(cu / Qs) + 1 its segments end
 // before the next one's first place; places in between have nothing to do.
-// Searched by one warp, 32 sequences at a time.
-__device__ __forceinline__ bool find_segment(const SsdPackedParams &p, int64_t place, int lane, Segment &g)
+// Up to 32 sequences are looked up together, one per lane, with their slots and
+// in one round of loads (a CTA starts with it); more are searched 32 at a time.
+// slot: the sequence's cache slot, -1 when it is skipped. Called by whole blocks.
+__device__ __forceinline__ bool find_segment(const SsdPackedParams &p, int64_t place, int lane, Segment &g, int &slot)
 {
-    const int T = (int)p.tokens;
-    if (p.seg_chunks == 0) {
-        // up to 32 sequences: the longest first, so that the last CTAs to start are short
-        int s = (int)place;
-        if (p.nseq <= 32) {
-            int len = -1, rank = 0;
-            if (lane < p.nseq) {
-                const SeqRange q = seq_range(p.cu, lane, p.tokens);
-                len = q.end - q.begin;
-            }
-            for (int j = 0; j < (int)p.nseq; ++j) {
+    const int T = (int)p.tokens, n = (int)p.nseq;
+    const int Qs = p.seg_chunks * kQ;
+    if (n <= 32) {
+        SeqRange q{0, 0};
+        int idx = lane;
+        if (lane < n) {
+            q = seq_range(p.cu, lane, p.tokens);
+            if (p.idx) idx = __ldg(p.idx + lane);
+        }
+        int s, len = q.end - q.begin;
+        if (Qs == 0) {
+            // the longest first, so that the last CTAs to start are short
+            int rank = 0;
+            for (int j = 0; j < n; ++j) {
                 const int other = __shfl_sync(0xffffffffu, len, j);
                 rank += other > len || (other == len && j < lane);
             }
-            s = __ffs(__ballot_sync(0xffffffffu, lane < p.nseq && rank == (int)place)) - 1;
+            s = __ffs(__ballot_sync(0xffffffffu, lane < n && rank == (int)place)) - 1;
+        } else {
+            s = __popc(__ballot_sync(0xffffffffu, lane < n && (int64_t)(q.begin / Qs) + lane <= place)) - 1;
         }
-        const SeqRange q = seq_range(p.cu, s, p.tokens);
-        g = {s, q.begin, q.end - q.begin, 0, 1, place};
-        return true;
+        s = max(s, 0);
+        const int begin = __shfl_sync(0xffffffffu, q.begin, s);
+        len = __shfl_sync(0xffffffffu, len, s);
+        slot = __shfl_sync(0xffffffffu, idx, s);
+        const bool twin = __any_sync(0xffffffffu, lane < s && idx == slot);   // (an earlier sequence's)
+        if (!p.state && !p.idx) slot = 0;
+        else if (slot < 0 || slot >= p.slots || twin) slot = -1;
+        g = {s, begin, len, 0, 1, place};
+    } else {
+        int lo = (int)place;
+        if (Qs > 0) {
+            lo = 0;
+            for (int m = n; m > 1;) {
+                const int step = (m + 31) / 32, c = lane * step;
+                bool le = false;
+                if (c < m) le = (int64_t)(min(max(__ldg(p.cu + lo + c), 0), T) / Qs) + lo + c <= place;
+                const int k = max(__popc(__ballot_sync(0xffffffffu, le)) - 1, 0);
+                lo += k * step;
+                m = min(step, m - k * step);
+            }
+        }
+        const SeqRange q = seq_range(p.cu, lo, p.tokens);
+        g = {lo, q.begin, q.end - q.begin, 0, 1, place};
+        slot = p.state || p.idx ? block_slot(p.idx, lo, p.slots) : 0;
     }
-    const int Qs = p.seg_chunks * kQ;
-    int lo = 0, n = (int)p.nseq;
-    while (n > 1) {
-        const int step = (n + 31) / 32, c = lane * step;
-        bool le = false;
-        if (c < n) le = (int64_t)(min(max(__ldg(p.cu + lo + c), 0), T) / Qs) + lo + c <= place;
-        const int k = max(__popc(__ballot_sync(0xffffffffu, le)) - 1, 0);
-        lo += k * step;
-        n = min(step, n - k * step);
-    }
-    const SeqRange q = seq_range(p.cu, lo, p.tokens);
-    const int64_t base = (int64_t)(q.begin / Qs) + lo;
-    const int len = q.end - q.begin;
-    const int64_t seg = place - base;
-    const int nseg = len > 0 ? (len + Qs - 1) / Qs : 1;
-    if (seg < 0 || seg >= nseg) return false;
-    g = {lo, q.begin + (int)seg * Qs, min(len - (int)seg * Qs, Qs), (int)seg, nseg, base};
+    if (Qs == 0) return true;
+    g.base = (int64_t)(g.row / Qs) + g.seq;
+    const int64_t seg = place - g.base;
+    g.nseg = g.len > 0 ? (g.len + Qs - 1) / Qs : 1;
+    if (seg < 0 || seg >= g.nseg) return false;
+    g.seg = (int)seg;
+    g.row += g.seg * Qs;
+    g.len = min(g.len - g.seg * Qs, Qs);
     return true;
 }
 
@@ -376,11 +395,8 @@ __device__ __forceinline__ bool setup(const SsdPackedParams &p, uint8_t *smem, u
         if (threadIdx.x == 0) atomicExch(p.status, (int)MS_ERR_ALIGNMENT);
         return false;
     }
-    bool have = find_segment(p, place, lane, g);
-    have = have && (last_too || g.seg + 1 < g.nseg);
-    if (!have) return false;   // (the same for every thread)
-    slot = p.state || p.idx ? block_slot(p.idx, g.seq, p.slots) : 0;
-    if (slot < 0) return false;
+    // (the same for every thread)
+    if (!find_segment(p, place, lane, g, slot) || slot < 0 || !(last_too || g.seg + 1 < g.nseg)) return false;
     if (threadIdx.x == 0) {
         auto init = [&](int b, int count) { mbar_init(base + off_bar + 8u * (uint32_t)b, (uint32_t)count); };
         for (int b : {kXFull0, kXFull1, kGFull, kSFull, kYFull, kDrain}) init(b, 1);
@@ -924,6 +940,14 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
             }
             give(kMReady);
 
+            const int64_t row = (int64_t)g.row + k * kQ + r;
+            uint4 zq[GATE ? 4 : 1];   // the gate of this thread's outputs, on its way early
+            if (GATE && live) {
+                const uint4 *zp =
+                    reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.z) + row * p.z_st + col);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) zq[GATE ? q : 0] = __ldg(zp + q);
+            }
             wait(kSFull, k & 1);
             if (k + 1 < K) wait(kStep0 + 2 * step_of(k + 1) + head, step_phase(k + 1));
             {
@@ -945,19 +969,17 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kYFree));
             if (live) {
-                const int64_t row = (int64_t)g.row + k * kQ + r;
                 uint32_t o[16];
                 if (GATE) {
-                    const uint4 *zp =
-                        reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.z) + row * p.z_st + col);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         float2 z[4];
-                        widen8(__ldg(zp + q), z);
+                        widen8(zq[GATE ? q : 0], z);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            y[8 * q + 2 * e] *= z[e].x * sigmoid(z[e].x);
-                            y[8 * q + 2 * e + 1] *= z[e].y * sigmoid(z[e].y);
+                            const float2 t = mul2(f2(y[8 * q + 2 * e], y[8 * q + 2 * e + 1]), mul2(z[e], sigmoid2(z[e])));
+                            y[8 * q + 2 * e] = t.x;
+                            y[8 * q + 2 * e + 1] = t.y;
                         }
                     }
                 }
