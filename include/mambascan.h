@@ -681,10 +681,17 @@ typedef struct ms_ssd_packed_args {
 ms_status mamba_ssd_packed_workspace_size(const ms_ssd_packed_args *args, size_t *bytes);
 
 /*
- * One or two kernel launches on `stream`. The workspace (256-byte aligned, of
- * at least mamba_ssd_packed_workspace_size bytes) starts with a status word
- * with mamba_ssd_fwd's meaning: 0 after a normal run, MS_ERR_TIMEOUT when an
- * internal wait gave up (outputs and states are then incomplete).
+ * One kernel launch on `stream`, or three when sequences are cut. The workspace
+ * (256-byte aligned, of at least mamba_ssd_packed_workspace_size bytes) starts
+ * with a status word with mamba_ssd_fwd's meaning: 0 after a normal run,
+ * MS_ERR_TIMEOUT when an internal wait gave up (outputs and states then hold
+ * wrong values). Calls that may overlap need workspaces of their own.
+ * Rounding: y is formed from operands rounded to bf16 once (the decay mask times
+ * C B^T, and the state that C reads); the states stay float32, accurate to about
+ * 2^-16 of the sum of the absolute values they are made of. One token's decay
+ * exp(delta A) below 2^-160 counts as 2^-160. An infinity or NaN in x spreads
+ * over the rows of its head and chunk of 128 tokens (0 times it is added
+ * there), and to the rows behind; other sequences are not touched.
  */
 ms_status mamba_ssd_packed_fwd(const ms_ssd_packed_args *args, void *workspace, size_t workspace_bytes,
                                void *stream);

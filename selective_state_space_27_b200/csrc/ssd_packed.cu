@@ -230,17 +230,21 @@ __device__ __forceinline__ bool find_segment(const SsdPackedParams &p, int64_t p
     return true;
 }
 
-// The step inputs of tokens t .. t + 3 of a segment of len tokens (0 behind its end).
-__device__ __forceinline__ void load_steps(const uint16_t *dt, int64_t stride, int t, int len, float (&v)[4])
+// The step inputs (bf16 bits) of tokens t .. t + 3 of a segment of len tokens, 0
+// behind its end. Kept as loaded: widening them here would wait for the loads.
+__device__ __forceinline__ void load_steps(const uint16_t *dt, int64_t stride, int t, int len, uint16_t (&v)[4])
 {
     const uint16_t *at = dt + t * stride;
 #pragma unroll
-    for (int j = 0; j < 4; ++j, at += stride) v[j] = t + j < len ? __uint_as_float((uint32_t)__ldg(at) << 16) : 0.f;
+    for (int j = 0; j < 4; ++j, at += stride) {
+        v[j] = 0;
+        if (t + j < len) v[j] = __ldg(at);
+    }
 }
 
-__device__ __forceinline__ float delta_of(const SsdPackedParams &p, float dt, float bias)
+__device__ __forceinline__ float delta_of(const SsdPackedParams &p, uint16_t dt, float bias)
 {
-    const float v = dt + bias;
+    const float v = __uint_as_float((uint32_t)dt << 16) + bias;
     return p.softplus ? softplus_fine(v) : v;
 }
 
@@ -431,9 +435,10 @@ __device__ __forceinline__ void teardown(uint32_t tmem)
 // zero for the others, and its decay. Chunks run from the segment's end to its
 // start: the decay of what follows a chunk is then a sum that ends at the
 // segment's end, the weights count to there and the chunks' products add up
-// without rescaling. Its barriers: xfull0 X, gfull / yfull B (by buffer), wready,
-// step (by buffer and head) and sfree (by buffer: the products of the chunk are
-// done) as above; each one's next phase needs what its waiters do next.
+// without rescaling. Its barriers: xfull0 X, mready X read, gfull / yfull B (by
+// buffer), wready, step (by buffer and head) and sfree (by buffer: the products of
+// the chunk are done) as above; each one's next phase needs what its waiters do
+// next.
 __global__ void __launch_bounds__(kThreads, 1)
 ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap b_map,
                          const SsdPackedParams p)
@@ -463,8 +468,9 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
             const uint16_t *dtp = reinterpret_cast<const uint16_t *>(p.dt) + (int64_t)g.row * p.dt_st + h;
             // Two chunks at a time: the sums' shuffles wait for each other, and behind the
             // products' operand reads; those of two chunks overlap.
-            float dtv[2][4], after = 0.f;   // the step inputs of the next two chunks; decay behind them
-            auto fetch = [&](int i, float (&v)[4]) {
+            uint16_t dtv[2][4];   // the step inputs of the next two chunks
+            float after = 0.f;    // decay behind them
+            auto fetch = [&](int i, uint16_t (&v)[4]) {
                 if (i < K) load_steps(dtp, p.dt_st, (K - 1 - i) * kQ + 4 * lane, g.len, v);
             };
             fetch(0, dtv[0]);
@@ -508,7 +514,7 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
                 tma_load_2d(b, &b_map, full, hp.group * kN, row);
                 tma_load_2d(b + kAtom, &b_map, full, hp.group * kN + 64, row);
             }
-            if (i > 0) wait(kWReady, (i - 1) & 1);
+            if (i > 0) wait(kMReady, (i - 1) & 1);
             if (lane == 0) {
                 mbar_arrive_tx(bar(kXFull0), (uint32_t)hp.nh * kAtom);
                 for (int j = 0; j < hp.nh; ++j) {
@@ -545,16 +551,22 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
         for (int i = 0; i < K; ++i) {
             wait(kStep0 + 2 * (i & 1) + head, phase(i));
             wait(kXFull0, i & 1);
-            if (i >= 2) wait(kSFree0 + (i & 1), phase(i - 2));
             const float w = step[2 * (i & 1) + head].w[r];
             const uint32_t tiles = (uint32_t)(2 * (i & 1) + head) * kAtom;
+            uint4 x[4];
 #pragma unroll
-            for (int q = 4 * hq; q < 4 * hq + 4; ++q) {
-                const uint32_t at = sw128((uint32_t)r, (uint32_t)q);
+            for (int q = 0; q < 4; ++q)
+                x[q] = ld_shared_v4(base + (uint32_t)head * kAtom + sw128((uint32_t)r, (uint32_t)(4 * hq + q)));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kMReady));   // X was read: the next chunk's may come
+            if (i >= 2) wait(kSFree0 + (i & 1), phase(i - 2));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t at = tiles + sw128((uint32_t)r, (uint32_t)(4 * hq + q));
                 uint32_t hi[4], lo[4];
-                split(ld_shared_v4(base + (uint32_t)head * kAtom + at), w, hi, lo);
-                st_shared_v4(base + kStW + tiles + at, hi[0], hi[1], hi[2], hi[3]);
-                st_shared_v4(base + kStL + tiles + at, lo[0], lo[1], lo[2], lo[3]);
+                split(x[q], w, hi, lo);
+                st_shared_v4(base + kStW + at, hi[0], hi[1], hi[2], hi[3]);
+                st_shared_v4(base + kStL + at, lo[0], lo[1], lo[2], lo[3]);
             }
             async_proxy_fence();
             __syncwarp();
@@ -700,7 +712,7 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
         if (head < hp.nh) {
             const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
             const uint16_t *dtp = reinterpret_cast<const uint16_t *>(p.dt) + (int64_t)g.row * p.dt_st + h;
-            float dtv[4];   // the step inputs of the next chunk
+            uint16_t dtv[4];   // the step inputs of the next chunk
             load_steps(dtp, p.dt_st, 4 * lane, g.len, dtv);
             for (int k = 0; k < K; ++k) {
                 if (k >= kSteps) wait(kSFree0 + step_of(k), step_phase(k - kSteps));
