@@ -8,9 +8,14 @@
 // float32 operations per element: bound by HBM bandwidth. A thread owns four
 // channels and slides a window of W inputs down the tokens in registers, so an
 // input is loaded once per tile of tokens plus W - 1 look-back rows per tile.
-// Measured on B200 for 24000 tokens x 4352 channels, bf16, W = 4: 89 us (72% of
-// the measured copy bandwidth); 117 us with eight channels per thread (too few
-// warps), 104 us with eight tiles per thread instead of one stretch of rows.
+// Measured on B200 for 24000 tokens x 4352 channels, bf16, W = 4: 85 us (75% of
+// the measured copy bandwidth); 89 us with blocks of 256 threads instead of 64
+// (28 warps per SM fit instead of 32), 117 us with eight channels per thread (too
+// few warps), 89 us with two (1280 threads per SM, twice the rows in flight),
+// 104 us with eight tiles per thread instead of one stretch of rows, 104 and 135 us
+// with two and eight rows loaded ahead instead of four. The special function unit
+// is 59% busy (exponential and reciprocal of the SiLU); the rest is the latency
+// of loads at the 64 registers per thread that 32 warps leave.
 //
 // Two kinds of work. A tile is a stretch of consecutive rows of the packed
 // stream, whatever sequences they belong to, except each sequence's first
@@ -25,7 +30,7 @@
 namespace ms {
 namespace {
 
-constexpr int kMaxThreads = 256;
+constexpr int kMaxThreads = 64;
 constexpr int kThreadsPerSm = 1024;        // threads that run together on an SM
 
 template <typename T, int VEC, int W>
