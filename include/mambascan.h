@@ -630,6 +630,7 @@ ms_status mamba_scan_fwd_noalloc(const ms_scan_args *args, void *stream);
  *   state : (slots, width - 1, channels) in_dtype, updated in place; entry and
  *           row strides given. Unused (NULL) when width is 1.
  * cu_seqlens NULL is the single-token form: tokens == nseq, sequence s is row s.
+ * y must not overlap x (a row is read again for the rows behind it and the state).
  */
 typedef struct ms_conv_packed_args {
     int64_t tokens, channels, nseq, slots;
@@ -650,9 +651,11 @@ ms_status mamba_conv_packed_fwd(const ms_conv_packed_args *args, const ms_conv1d
  *   x, z, y : (tokens, nheads, 64), dt : (tokens, nheads),
  *   B, C    : (tokens, ngroups, 128); token strides given, inner axes contiguous
  *   state   : (slots, nheads, 64, 128) float32, updated in place; slot stride
- *             given (a multiple of 4), inner axes contiguous, 16-byte aligned
- * Alignment as in mamba_ssd_fwd. max_seqlen: the longest sequence as far as the
- * host knows it (0: not known); it steers the schedule only.
+ *             given, inner axes contiguous
+ * x, y, z, B and C are 16-byte aligned with token strides that are multiples of
+ * 8 elements. y may be x or z itself, but overlap no other input. max_seqlen: the
+ * longest sequence as far as the host knows it (0: not known); it steers the
+ * schedule only.
  */
 typedef struct ms_ssd_packed_args {
     int64_t tokens, nseq, nheads, ngroups, slots, max_seqlen;
@@ -734,7 +737,8 @@ ms_status mamba_ssd_state_update(const ms_ssd_update_args *args, void *stream);
  * (residual, residual_scale); the norm after the Mamba-2 scan takes the gate
  * (z, groups). x, z, y, dy: in_dtype; residual and residual_out:
  * residual_dtype, which is in_dtype or MS_F32. Row strides given, channels
- * contiguous. weight: (dim) float32.
+ * contiguous. weight: (dim) float32. y may be x or z itself, and residual_out
+ * residual; the outputs overlap no other input.
  */
 typedef struct ms_norm_args {
     int64_t rows, dim, group_size;
@@ -755,11 +759,12 @@ ms_status mamba_norm_fwd(const ms_norm_args *args, void *stream);
  * Gradients of mamba_norm_fwd for the loss sum(y dy) + sum(residual_out
  * dresidual_out). In `fwd`, y and residual are not used: residual_out says by
  * being given whether the forward had a residual, and the sum is read from it
- * as the forward stored it. x is then read only for a gate that comes first. dweight (dim) float32 may be NULL.
- * dx and dz have in_dtype, dresidual and dresidual_out (NULL = zero)
- * residual_dtype. dz is required with z, dresidual with residual_out. The
- * sums over the rows are taken in a fixed order. The workspace (16-byte
- * aligned) is needed for dweight only.
+ * as the forward stored it. x is then read only for a gate that comes first.
+ * dweight (dim) float32 may be NULL. dx and dz have in_dtype, dresidual and
+ * dresidual_out (NULL = zero) residual_dtype. dz is required with z, dresidual
+ * with residual_out. The gradients must not overlap the inputs. The sums over
+ * the rows are taken in a fixed order. The workspace (16-byte aligned) is needed
+ * for dweight only.
  */
 typedef struct ms_norm_bwd_args {
     const void *dy;             int64_t dy_row_stride;

@@ -768,6 +768,7 @@ ms_status mamba_conv_packed_fwd(const ms_conv_packed_args *a, const ms_conv1d_ar
     if (!a->cu_seqlens && c->width > 1 && !a->state) return invalid("single tokens need a state");
     if (a->nseq > (int64_t(1) << 30)) return invalid("nseq above 2^30");
     if (a->tokens > 0 && (!a->x || !a->y)) return invalid("x and y are required");
+    if (a->tokens > 0 && a->x == a->y) return invalid("the convolution is not computed in place: y must not be x");
     if (a->x_token_stride < 0 || a->y_token_stride < a->channels ||
         (stateful && (a->state_slot_stride < 0 || a->state_row_stride < a->channels)))
         return invalid("strides must be non-negative and those of y and the state rows cover the channels");

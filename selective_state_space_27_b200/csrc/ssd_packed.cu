@@ -125,9 +125,10 @@ __device__ __forceinline__ int step_of(int k) { return k & (kSteps - 1); }
 __device__ __forceinline__ uint32_t step_phase(int k) { return (uint32_t)(k / kSteps) & 1u; }
 
 // A bounded wait. When its limit runs out it records that in the status word and
-// raises the CTA's abort flag; from then on every wait of the CTA returns at once
-// and the roles run to their end on what is there: all addresses stay in bounds,
-// and the loads and MMAs in flight are still waited for before the CTA leaves.
+// raises the CTA's abort flag; from then on every wait of the CTA returns at once,
+// no more loads are issued and the other roles run to their end on what is there:
+// all addresses stay in bounds, and the loads and MMAs in flight are still waited
+// for before the CTA leaves.
 // The slow path is a call: the loops wait in many places and their code has to
 // stay small for the instruction cache.
 __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status,
@@ -154,6 +155,13 @@ struct Waiter {
     {
         one(b, parity);
         __syncwarp();
+    }
+    // for the loading warp: false when the CTA has given up. It then issues nothing
+    // more: a load is announced only on a barrier whose last phase has completed.
+    __device__ __forceinline__ bool go(int b, uint32_t parity) const
+    {
+        one(b, parity);
+        return __all_sync(0xffffffffu, !*abort_flag);
     }
 };
 
@@ -505,16 +513,18 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
             if (lane == 0) p.seg_decay[place * p.nheads + h] = after;
         }
     } else if (warp == kTmaWarp) {
+        int bs = 0, xs = 0;   // chunks whose B, and whose X, are on their way
         for (int i = 0; i < K; ++i) {
             const int row = g.row + (K - 1 - i) * kQ;
-            if (i >= 2) wait(kSFree0 + (i & 1), phase(i - 2));
+            if (i >= 2 && !wait.go(kSFree0 + (i & 1), phase(i - 2))) break;
             if (lane == 0) {
                 const uint32_t full = bar(bfull(i)), b = base + kStB + (uint32_t)(2 * (i & 1)) * kAtom;
                 mbar_arrive_tx(full, 2 * kAtom);
                 tma_load_2d(b, &b_map, full, hp.group * kN, row);
                 tma_load_2d(b + kAtom, &b_map, full, hp.group * kN + 64, row);
             }
-            if (i > 0) wait(kMReady, (i - 1) & 1);
+            bs = i + 1;
+            if (i > 0 && !wait.go(kMReady, (i - 1) & 1)) break;
             if (lane == 0) {
                 mbar_arrive_tx(bar(kXFull0), (uint32_t)hp.nh * kAtom);
                 for (int j = 0; j < hp.nh; ++j) {
@@ -522,11 +532,12 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
                     if (i + 1 < K) tma_prefetch_2d(&x_map, (hp.h + j) * kP, row - kQ);
                 }
             }
+            xs = i + 1;
             __syncwarp();
         }
         if (lane == 0) {   // loads in flight must land
-            mbar_wait(bar(kXFull0), (K - 1) & 1);
-            for (int i = max(0, K - 2); i < K; ++i) mbar_wait(bar(bfull(i)), phase(i));
+            if (xs) mbar_wait(bar(kXFull0), (xs - 1) & 1);
+            for (int i = max(0, bs - 2); i < bs; ++i) mbar_wait(bar(bfull(i)), phase(i));
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -742,7 +753,7 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
         }
     } else if (warp == kTmaWarp) {
         // ---- loads, each as soon as its buffer was read for the last time ----
-        int cs = 0, xs = 0;   // chunks whose C, and whose X, are on their way
+        int cs = 0, bs = 0, xs = 0;   // chunks whose C, B and X are on their way
         auto load_bc = [&](const CUtensorMap *map, uint32_t tile, int k) {
             if (lane == 0) {
                 const int row = g.row + k * kQ, col = hp.group * kN;
@@ -771,27 +782,28 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
             }
             xs = k + 1;
         };
+        bool ok = true;
         for (int k = -1; k + 1 < K; ++k) {
-            if (k >= 0) wait(kGFull, k & 1);
+            if (k >= 0 && !(ok = wait.go(kGFull, k & 1))) break;
             load_bc(&c_map, base + kOffC, k + 1);
             cs = k + 2;
-            if (k >= 0) wait(kSFull, k & 1);
+            if (k >= 0 && !(ok = wait.go(kSFull, k & 1))) break;
             load_bc(&b_map, base + kOffB, k + 1);
+            bs = k + 2;
             if (k < 0) {
                 load_x(0);
                 if (K > 1) load_x(1);
             } else {
                 // y of chunk k (a full one) from X's place, then X of chunk k + 2 there
-                wait(kYStore0 + (k & 1), (uint32_t)(k >> 1) & 1u);
+                if (!(ok = wait.go(kYStore0 + (k & 1), (uint32_t)(k >> 1) & 1u))) break;
                 store_y(k);
                 if (k + 2 < K) load_x(k + 2);
             }
         }
-        if (K > 0 && g.len >= K * kQ) {
-            wait(kYStore0 + ((K - 1) & 1), (uint32_t)((K - 1) >> 1) & 1u);
+        if (ok && K > 0 && g.len >= K * kQ && wait.go(kYStore0 + ((K - 1) & 1), (uint32_t)((K - 1) >> 1) & 1u))
             store_y(K - 1);
-        }
-        if (lane == 0) {   // loads in flight must land (after a timeout a phase with C but no B runs its limit out)
+        if (lane == 0) {   // loads in flight must land
+            if (cs > bs) mbar_arrive(bar(kFull));   // (given up between the two: C's phase ends without B)
             if (cs) mbar_wait(bar(kFull), (uint32_t)(cs - 1) & 1u);
             for (int k = max(0, xs - 2); k < xs; ++k) mbar_wait(bar(kXFull0 + (k & 1)), (uint32_t)(k >> 1) & 1u);
         }

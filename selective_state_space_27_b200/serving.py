@@ -250,6 +250,8 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
     if headdim != SSD_HEADDIM:
         raise ValueError(f"x must be (tokens, nheads, {SSD_HEADDIM})")
     cu, nseq = _offsets(cu_seqlens, device)
+    if B.dim() != 3:
+        raise ValueError(f"B must be (tokens, ngroups, {SSD_DSTATE})")
     y = x.new_empty(shape) if out is None else out
     bc = (tokens, B.shape[1], SSD_DSTATE)
     idx, flags = _slots(nseq, state_indices, has_initial_state, device)

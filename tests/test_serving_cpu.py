@@ -76,6 +76,11 @@ def test_conv_packed_refuses(lib, change, status):
     assert lib.mamba_conv_packed_fwd(ctypes.byref(conv_args(**change)), ctypes.byref(conv_filter()), None) == status
 
 
+def test_conv_packed_refuses_in_place(lib):
+    assert lib.mamba_conv_packed_fwd(ctypes.byref(conv_args(y=BASE)), ctypes.byref(conv_filter()), None) == 1
+    assert b"in place" in lib.mamba_last_error()
+
+
 @pytest.mark.parametrize("change,status", [(dict(weight=None), 1), (dict(width=0), 1), (dict(width=5), 2),
                                            (dict(silu=2), 1), (dict(weight=BASE + 2), 3)])
 def test_conv_packed_refuses_filters(lib, change, status):

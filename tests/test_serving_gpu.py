@@ -269,6 +269,66 @@ def test_ssd_packed_no_tokens(ms):
     assert torch.equal(state[1:], before[1:]) and not state[0].any()
 
 
+def test_ssd_packed_longest_is_a_hint(ms):
+    """A max_seqlen that is too small, exact or too large changes the schedule, not what is computed."""
+    g = rng(41)
+    cu, cu_t = offsets([2500, 40, 700])
+    a, kw, _ = ssd_inputs(g, cu[-1], 2, 1, False)
+    y = torch.zeros(cu[-1], 2, 64, dtype=torch.bfloat16, device="cuda")
+    first = normal(g, 3, 2, 64, 128)
+    want, new, ymag, smag = ref.ssd(*a.values(), cu, state=first, init=[True] * 3, y=y, **kw)
+    for longest in (1, 300, 1000, 2500, 10 ** 6):
+        state = first.clone()
+        got = ms.ssd_packed_fwd(*a.values(), cu_t, state=state, max_seqlen=longest,
+                                has_initial_state=torch.ones(3, dtype=torch.bool, device="cuda"), **kw)
+        ssd_close(got, state, want, new, ymag, smag)
+
+
+@pytest.mark.parametrize("lens", [[300, 77], [3000]])
+def test_ssd_packed_in_place(ms, lens):
+    """y in the place of x, and of z."""
+    g = rng(43)
+    _, cu = offsets(lens)
+    for name in ("x", "z"):
+        a, kw, _ = ssd_inputs(g, sum(lens), 2, 1, True)
+        want = ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=max(lens), **kw)
+        out = a["x"] if name == "x" else kw["z"]
+        got = ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=max(lens), out=out, **kw)
+        assert got is out and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("lens,H", [([2000, 300], 4), ([40000], 2)])
+def test_ssd_packed_reports_a_wait_that_ran_out(ms, lens, H):
+    """A limit of a microsecond, shorter than a load takes: the call ends, says so and leaves nothing behind."""
+    g = rng(47)
+    _, cu = offsets(lens)
+    a, kw, _ = ssd_inputs(g, sum(lens), H, 1, False)
+    want = ms.ssd_packed_fwd(*a.values(), cu, **kw)
+    with pytest.raises(ms.MambaScanError) as e:
+        ms.ssd_packed_fwd(*a.values(), cu, wait_limit_us=1, **kw)
+    assert e.value.status == 5                           # MS_ERR_TIMEOUT
+    assert torch.equal(ms.ssd_packed_fwd(*a.values(), cu, **kw), want)
+
+
+def test_cache_beyond_32_bits(ms):
+    """Slots whose offset in the cache passes 2^31 elements (8 GB of states)."""
+    g = rng(53)
+    H, slots = 64, 4100                                      # 524288 values per slot
+    state = torch.empty(slots, H, 64, 128, device="cuda")
+    small = torch.zeros(2, H, 64, 128, device="cuda")
+    at = [4099, 4097]
+    a, kw, _ = ssd_inputs(g, 40, H, 1, False)
+    kw.pop("z")
+    _, cu = offsets([30, 10])
+    want = ms.ssd_packed_fwd(*a.values(), cu, state=small, **kw)
+    got = ms.ssd_packed_fwd(*a.values(), cu, state=state, state_indices=i32(at), **kw)
+    assert torch.equal(got, want) and torch.equal(state[at], small)
+    token = [t[:2] if t.dim() > 1 else t for t in a.values()]
+    want = ms.ssd_state_update(small, *token, **kw)
+    got = ms.ssd_state_update(state, *token, state_indices=i32(at), **kw)
+    assert torch.equal(got, want) and torch.equal(state[at], small)
+
+
 def test_ssd_packed_agrees_with_the_dense_forward(ms):
     """Equal lengths: the same layer through ssd_fwd, whose operands are rounded alike."""
     g = rng(21)
@@ -389,6 +449,21 @@ def test_norm_bwd_against_differences(ms):
             diff = ((loss(*up) - loss(*down)) / (2 * h)).item()
             # the difference's own error is about h^2 times a third derivative
             assert abs(got[name].view(-1)[j].item() - diff) <= 1e-4 * (1 + abs(diff))
+
+
+@pytest.mark.parametrize("rows,dim,group", [(40, 64, 16), (9, 2048, 2048), (3, 40000, 40000)])
+def test_norm_in_place(ms, rows, dim, group):
+    """y in the place of x or z, the sum in the residual's."""
+    g = rng(dim)
+    x, z, w = normal(g, rows, dim), normal(g, rows, dim), normal(g, dim)
+    res = normal(g, rows, dim)
+    kw = dict(weight=w, group_size=group)
+    want, sums = ms.norm_fwd(x, z=z, residual=res, **kw)
+    for name in ("x", "z"):
+        c = dict(x=x.clone(), z=z.clone(), residual=res.clone())
+        y, ro = ms.norm_fwd(**c, **kw, out=c[name], residual_out=c["residual"])
+        assert y is c[name] and ro is c["residual"]
+        assert torch.equal(y, want) and torch.equal(ro, sums)
 
 
 def test_norm_rows_none(ms):
