@@ -14,6 +14,13 @@
 // backward a team stays on one group of channels and walks down the rows of
 // its slab, so that its share of dw stays in registers; the slabs' shares are
 // added by a second kernel.
+// Measured on B200 for 16384 rows x 8 groups of 512, bf16, gated: forward 73 us
+// (84% of the measured copy bandwidth), backward 138 us (75%: 128 registers leave
+// 16 warps per SM, whose loads come in bursts between the rows' reductions); 4099
+// rows x 1530, float32, with a residual: backward 31 us (62%, 6 us of it the
+// second kernel's). Taking the gate's two reciprocals of a pair from one of their
+// product, to relieve the special function unit (56% busy in the forward), made
+// all of them slower: 86 and 158 us.
 #include <type_traits>
 
 #include "launch.h"

@@ -41,6 +41,20 @@
 // second one adds these up along each sequence, a third one does the rest from
 // the state that its segment starts from. Three launches on one stream: no CTA
 // waits for another.
+//
+// Measured on B200, bf16: 16 ragged prompts of 24000 tokens, 64 heads, half of
+// them resumed, 182 us (38% of the time its bytes take; the longest prompts first,
+// so the SMs end within 3% of each other); 4 x 8192 tokens x 64 heads 237 us (the
+// dense kernel, one head per CTA: 385 us); one prompt of 32768 tokens x 24 heads
+// 143 us in segments, 44 + 8 + 95 us; three prompts of 378 tokens x 24 heads
+// 18.5 us on the device. A chunk of a pair of heads takes about 6800 clocks, of
+// which the tensor core works 3072. What bounds it is the chain w X - state
+// product - next state - C H^T together with shared memory, which is about 75%
+// busy with the products' operands (2304 clocks), TMA (1024) and the arithmetic
+// warps' own accesses (1800), so that arithmetic beside the products slows both.
+// Measured and not kept (4 x 8192 x 64 heads, against 240 us): C H^T issued before
+// G 259 us; w X made while M' X runs 249 us; X kept in registers 241 us (spills);
+// one head per CTA and two CTAs per SM 298 us; w X shared out unevenly 271 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
