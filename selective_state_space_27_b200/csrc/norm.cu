@@ -15,9 +15,11 @@
 // its slab, so that its share of dw stays in registers; the slabs' shares are
 // added by a second kernel.
 // Measured on B200 for 16384 rows x 8 groups of 512, bf16, gated: forward 73 us
-// (84% of the measured copy bandwidth), backward 138 us (75%: 128 registers leave
-// 16 warps per SM, whose loads come in bursts between the rows' reductions); 4099
-// rows x 1530, float32, with a residual: backward 31 us (62%, 6 us of it the
+// (84% of the measured copy bandwidth), backward 127 us (81%). 128 registers leave
+// the backward 16 warps per SM: with a row's loads in registers they came in bursts
+// between the reductions (137 us), so the next rows wait in shared memory, and the
+// row in work is read from there twice (once, held over the reduction: 130 us).
+// 4099 rows x 1530, float32, with a residual: backward 31 us (62%, 6 us of it the
 // second kernel's). Taking the gate's two reciprocals of a pair from one of their
 // product, to relieve the special function unit (56% busy in the forward), made
 // all of them slower: 86 and 158 us.
@@ -270,6 +272,50 @@ struct BwdVec {
         if (H::res(p)) sum = load_raw<R, VEC>(q.sum + i);
         if (H::res(p) && q.ds) ds = load_raw<R, VEC>(q.ds + i);
     }
+    // The same by way of shared memory, where the loads of the next rows wait without
+    // holding registers: a thread's pieces lie blockDim.x apart, it alone writes
+    // and reads them.
+    static constexpr int kT = VEC * (int)sizeof(T), kR = VEC * (int)sizeof(R);
+    static constexpr int kBytes = MODE == kResidual ? kT + 2 * kR : MODE == kPlain ? 2 * kT : 3 * kT;
+    static __device__ __forceinline__ void stage(uint32_t at, const BwdRow<T, R, VEC, MODE> &q, int64_t i) {
+        put<kT>(at, 0, q.dy + i);
+        if constexpr (MODE == kResidual) {
+            put<kR>(at, kT, q.sum + i);
+            if (q.ds) put<kR>(at, kT + kR, q.ds + i);
+        } else {
+            put<kT>(at, kT, q.x + i);
+            if constexpr (MODE != kPlain) put<kT>(at, 2 * kT, q.z + i);
+        }
+    }
+    __device__ __forceinline__ void fetch(uint32_t at, const BwdRow<T, R, VEC, MODE> &q) {
+        get<kT>(at, 0, &dy);
+        if constexpr (MODE == kResidual) {
+            get<kR>(at, kT, &sum);
+            if (q.ds) get<kR>(at, kT + kR, &ds);
+        } else {
+            get<kT>(at, kT, &x);
+            if constexpr (MODE != kPlain) get<kT>(at, 2 * kT, &z);
+        }
+    }
+    template <int N> static __device__ __forceinline__ void put(uint32_t at, int off, const void *src) {
+        constexpr int P = N < 16 ? N : 16;
+#pragma unroll
+        for (int o = 0; o < N; o += P)
+            cp_async_full<P>(at + (uint32_t)(off + o) * blockDim.x + threadIdx.x * P, static_cast<const char *>(src) + o);
+    }
+    template <int N> static __device__ __forceinline__ void get(uint32_t at, int off, void *dst) {
+        uint32_t *d = static_cast<uint32_t *>(dst);
+        if constexpr (N == 8) {
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(d[0]), "=r"(d[1])
+                         : "r"(at + (uint32_t)off * blockDim.x + threadIdx.x * 8u) : "memory");
+        } else {
+#pragma unroll
+            for (int o = 0; o < N; o += 16)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(d[o / 4]), "=r"(d[o / 4 + 1]), "=r"(d[o / 4 + 2]), "=r"(d[o / 4 + 3])
+                             : "r"(at + (uint32_t)(off + o) * blockDim.x + threadIdx.x * 16u) : "memory");
+        }
+    }
     // v, and dy as it reaches the norm's output (before the weight)
     __device__ __forceinline__ void values(const NormParams &p, float (&v)[VEC], float (&d)[VEC]) const {
         widen<T, VEC>(dy, d);
@@ -317,11 +363,22 @@ struct BwdVec {
     }
 };
 
+// Rows in shared memory per thread: the one in work and those on their way (0: the
+// rows are loaded into registers, for vectors below 8 bytes and for the threads
+// with the most bytes, whose rows would not fit twice). Gated bf16 groups of 512
+// have 96 bytes: 127 us with three rows, 129 with two, 127 with four; 192 bytes
+// (float32 with a residual): 34 us with two rows, 49 with three.
+template <typename T, typename R, int VEC, int NV, int MODE>
+constexpr int stages_of() {
+    constexpr int bytes = NV * BwdVec<T, R, VEC, MODE>::kBytes;
+    return MODE == kAny || bytes > 192 ? 0 : bytes > 96 ? 2 : 3;
+}
+
 // Block (slab, group): teams walk rows slab * teams + team, + slabs * teams, ...
 template <typename T, typename R, int VEC, int NV, bool BLOCK, int MODE>
 __global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarps * 32, BLOCK ? 1 : kBwdThreads / (kWarps * 32))
     norm_bwd_kernel(const NormParams p, const NormBwdParams g) {
-    extern __shared__ float dwsum[];   // warp teams: the group's share of dw
+    extern __shared__ __align__(16) float dwsum[];   // warp teams: the group's share of dw
     __shared__ float smem[64];
     const int ts = BLOCK ? (int)blockDim.x : p.team;
     const int teams = blockDim.x / ts, team = threadIdx.x / ts;
@@ -335,17 +392,46 @@ __global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarps * 32, BLOCK ? 1 : k
         for (int e = 0; e < VEC; ++e) w[i][e] = 1.f;
         if (p.w && lane + i * ts < nvec) load_f32<VEC>(p.w + c0 + (lane + i * ts) * VEC, w[i]);
     }
+    constexpr int S = stages_of<T, R, VEC, NV, MODE>();
+    using Vec = BwdVec<T, R, VEC, MODE>;
+    // (behind the share of dw)
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(dwsum) + (BLOCK ? 0u : (uint32_t)(p.gs + 3) / 4u * 16u);
+    auto slot = [&](int st, int i) { return ring + (uint32_t)((st * NV + i) * Vec::kBytes) * blockDim.x; };
+    auto stage_row = [&](int64_t r0, int st) {
+        if constexpr (S > 0) {
+            const int64_t row = r0 + team;
+            if (row < p.rows) {
+                const BwdRow<T, R, VEC, MODE> q(p, g, row, c0);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (lane + i * ts < nvec) Vec::stage(slot(st, i), q, (lane + i * ts) * VEC);
+            }
+            cp_async_commit();
+        }
+    };
+    const int64_t stride = g.slabs * teams;
+    int now = 0;   // the row's place in the ring
+    if constexpr (S > 0)
+#pragma unroll
+        for (int k = 0; k + 1 < S; ++k) stage_row(slab * teams + k * stride, k);
     // every team of a block makes the same number of rounds (the last ones on row 0, without effect)
-    for (int64_t r0 = slab * teams; r0 < p.rows; r0 += g.slabs * teams) {
+    for (int64_t r0 = slab * teams; r0 < p.rows; r0 += stride) {
         const int64_t row = r0 + team;
         const bool on = row < p.rows;
         const BwdRow<T, R, VEC, MODE> q(p, g, on ? row : 0, c0);
-        BwdVec<T, R, VEC, MODE> in[NV];
+        Vec in[NV];
+        if constexpr (S > 0) {
+            stage_row(r0 + (S - 1) * stride, now == 0 ? S - 1 : now - 1);
+            cp_async_wait<S - 1>();
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = lane + i * ts;
             in[i] = {};
-            if (on && j < nvec) in[i].load(p, q, j * VEC);
+            if (on && j < nvec) {
+                if constexpr (S > 0) in[i].fetch(slot(now, i), q);
+                else in[i].load(p, q, j * VEC);
+            }
         }
         float s[2] = {0.f, 0.f};
 #pragma unroll
@@ -366,12 +452,14 @@ __global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarps * 32, BLOCK ? 1 : k
             const int j = lane + i * ts;
             if (on && j < nvec) {
                 float v[VEC], d[VEC];
+                if constexpr (S > 0) in[i].fetch(slot(now, i), q);   // (once more: not held over the reduction)
                 in[i].values(p, v, d);
                 in[i].store(p, q, j * VEC, r, m, v, d, w[i]);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) dw[i][e] = fmaf(d[e], v[e] * r, dw[i][e]);
             }
         }
+        if constexpr (S > 0) now = now + 1 == S ? 0 : now + 1;
     }
     if (!g.partial) return;
     float *out = g.partial + slab * p.dim + c0;
@@ -572,12 +660,19 @@ cudaError_t bwd_vec(const NormParams &p0, const NormBwdParams &g, cudaStream_t s
         e = with_mode<T, R, VEC>(p, [&](auto mode) {
             return with_nv<VEC>(t.nv, [&](auto nv) {
                 constexpr int NV = decltype(nv)::value, MODE = decltype(mode)::value;
-                if (t.block)
-                    norm_bwd_kernel<T, R, VEC, NV, true, MODE><<<grid, t.ts, 0, stream>>>(p, g);
-                else
-                    norm_bwd_kernel<T, R, VEC, NV, false, MODE>
-                        <<<grid, kWarps * 32, static_cast<size_t>(p.gs) * sizeof(float), stream>>>(p, g);
-                return cudaGetLastError();
+                constexpr int row = stages_of<T, R, VEC, NV, MODE>() * NV * BwdVec<T, R, VEC, MODE>::kBytes;
+                const auto launch = [&](auto kernel, int threads, int64_t share) {
+                    const size_t smem = static_cast<size_t>(row) * threads + static_cast<size_t>(share + 3) / 4 * 16;
+                    if (smem > 48 * 1024) {
+                        const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                                   static_cast<int>(smem));
+                        if (a != cudaSuccess) return a;
+                    }
+                    kernel<<<grid, threads, smem, stream>>>(p, g);
+                    return cudaGetLastError();
+                };
+                if (t.block) return launch(norm_bwd_kernel<T, R, VEC, NV, true, MODE>, t.ts, 0);
+                return launch(norm_bwd_kernel<T, R, VEC, NV, false, MODE>, kWarps * 32, p.gs);
             });
         });
     }
