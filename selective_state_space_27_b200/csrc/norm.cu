@@ -25,6 +25,7 @@
 // all of them slower: 86 and 158 us.
 #include <type_traits>
 
+#include "dependent.cuh"
 #include "launch.h"
 #include "vec.cuh"
 
@@ -462,6 +463,7 @@ __global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarps * 32, BLOCK ? 1 : k
         if constexpr (S > 0) now = now + 1 == S ? 0 : now + 1;
     }
     if (!g.partial) return;
+    dependents_may_start();
     float *out = g.partial + slab * p.dim + c0;
     if constexpr (BLOCK) {
 #pragma unroll
@@ -546,6 +548,7 @@ __global__ void __launch_bounds__(kMaxBlock) norm_bwd_long_kernel(const NormPara
 // block (32 bytes of a row), 128 strided sums each, those by shuffles and warps.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *partial, float *dw, int64_t slabs, int64_t dim) {
     __shared__ float acc[32][8];
+    wait_for_previous();
     const int cx = threadIdx.x & 7, k = threadIdx.x >> 3;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + cx;
     float s = 0.f;
@@ -677,8 +680,8 @@ cudaError_t bwd_vec(const NormParams &p0, const NormBwdParams &g, cudaStream_t s
         });
     }
     if (e != cudaSuccess || !g.dw || g.partial == g.dw) return e;
-    norm_dw_kernel<<<static_cast<unsigned>((p.dim + 7) / 8), 1024, 0, stream>>>(g.partial, g.dw, g.slabs, p.dim);
-    return cudaGetLastError();
+    return launch_dependent(norm_dw_kernel, dim3(static_cast<unsigned>((p.dim + 7) / 8)), 1024, 0, stream,
+                            static_cast<const float *>(g.partial), g.dw, g.slabs, p.dim);
 }
 
 // Widest vectors (16 bytes of the input type, 8 of a float32 row, or single

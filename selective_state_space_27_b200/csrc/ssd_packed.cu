@@ -39,8 +39,9 @@
 // (ssd_packed_segment): a first kernel computes what every segment but a
 // sequence's last adds to the state from zero (the state product alone), a
 // second one adds these up along each sequence, a third one does the rest from
-// the state that its segment starts from. Three launches on one stream: no CTA
-// waits for another.
+// the state that its segment starts from. The kernels of a call follow each other
+// on the stream, each starting while the one in front of it ends; no CTA waits
+// for another one of its kernel.
 //
 // Measured on B200, bf16: 16 ragged prompts of 24000 tokens, 64 heads, half of
 // them resumed, 182 us (38% of the time its bytes take; the longest prompts first,
@@ -60,6 +61,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "dependent.cuh"
 #include "device_math.cuh"
 #include "launch.h"
 #include "mambascan.h"
@@ -150,7 +152,10 @@ __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile i
 {
     const uint64_t t0 = global_ns();
     while (!*abort_flag && !mbar_test(bar, parity))
-        if (global_ns() - t0 > limit_ns) give_up(status, abort_flag);
+        if (global_ns() - t0 > limit_ns) {
+            wait_for_previous();   // (the status word was cleared, or a kernel's failure is in it)
+            give_up(status, abort_flag);
+        }
 }
 
 struct Waiter {
@@ -418,6 +423,7 @@ __device__ __forceinline__ bool setup(const SsdPackedParams &p, uint8_t *smem, u
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (base & 1023u) {
+        wait_for_previous();
         if (threadIdx.x == 0) atomicExch(p.status, (int)MS_ERR_ALIGNMENT);
         return false;
     }
@@ -449,6 +455,7 @@ __device__ __forceinline__ void teardown(uint32_t tmem)
         tc_after_sync();
         tmem_free(tmem, kTmemCols);
     }
+    wait_for_previous();   // a kernel does not end before the one in front of it has
 }
 
 // ---- first kernel: what a segment adds to the state ---------------------------
@@ -474,7 +481,10 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
     Segment g;
     int slot;
     uint32_t tmem;
-    if (!setup(p, smem, base, kStBar, place, hp.nh, g, slot, tmem, false)) return;
+    if (!setup(p, smem, base, kStBar, place, hp.nh, g, slot, tmem, false)) {
+        wait_for_previous();
+        return;
+    }
     auto bar = [&](int i) { return base + kStBar + 8u * (uint32_t)i; };
     StateStep *step = reinterpret_cast<StateStep *>(smem + kStStep);
     const int K = (g.len + kQ - 1) / kQ;
@@ -598,6 +608,7 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
             if (lane == 0) mbar_arrive(bar(kWReady));
         }
         wait(kSFree0 + ((K - 1) & 1), phase(K - 1));
+        dependents_may_start();
         tc_after_sync();
         const float f = ex2(step[2 * ((K - 1) & 1) + head].decay);
         float v[32];
@@ -623,6 +634,8 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
 // sequence's segments: place m then holds the state after segment m.
 __global__ void __launch_bounds__(256) ssd_packed_pass_kernel(const SsdPackedParams p)
 {
+    wait_for_previous();
+    dependents_may_start();
     constexpr int kBlocks = kP * kN / 4 / 256;   // blocks per (sequence, head)
     const int64_t pair = blockIdx.x / kBlocks;
     const int part = (int)(blockIdx.x - pair * kBlocks);
@@ -708,6 +721,13 @@ __device__ __forceinline__ void build_mask(uint32_t tg, uint32_t tm, const StepD
     tmem_store16(tm + 16u * (uint32_t)j, m);
 }
 
+// The status word, cleared in front of a call's kernels: they start beside it.
+__global__ void ssd_packed_clear_kernel(int *status)
+{
+    dependents_may_start();
+    *status = 0;
+}
+
 // GATE: y is multiplied by silu(z) (its own kernel: the code of the loop has to
 // stay small for the instruction cache).
 template <bool GATE>
@@ -725,11 +745,20 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
     Segment g;
     int slot;
     uint32_t tmem;
-    if (!setup(p, smem, base, kOffBar, place, hp.nh, g, slot, tmem, true)) return;
+    if (!setup(p, smem, base, kOffBar, place, hp.nh, g, slot, tmem, true)) {
+        wait_for_previous();
+        return;
+    }
     auto bar = [&](int i) { return base + kOffBar + 8u * (uint32_t)i; };
     StepData *step = reinterpret_cast<StepData *>(smem + kOffStep);
     const int K = (g.len + kQ - 1) / kQ;
     const Waiter wait{base + kOffBar, reinterpret_cast<volatile int *>(smem + kOffBar + kOffTmem + 8), p.status, p.wait_limit_ns};
+
+    // (by every role in front of its first wait for another one that needs the segments'
+    // states: the time until these are there must not count as its wait)
+    auto after_states = [&] {
+        if (p.seg_chunks) wait_for_previous();
+    };
 
     if (warp == kStepWarp || warp == kStepWarp + 1) {
         // ---- step data of one head, up to kSteps chunks ahead ----
@@ -740,6 +769,7 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
             uint16_t dtv[4];   // the step inputs of the next chunk
             load_steps(dtp, p.dt_st, 4 * lane, g.len, dtv);
             for (int k = 0; k < K; ++k) {
+                if (k == kSteps) after_states();
                 if (k >= kSteps) wait(kSFree0 + step_of(k), step_phase(k - kSteps));
                 float d[4], a[4], pre[4], suf[4], all, cf[4], w[4];
 #pragma unroll
@@ -798,6 +828,7 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
         };
         bool ok = true;
         for (int k = -1; k + 1 < K; ++k) {
+            if (k == 0) after_states();
             if (k >= 0 && !(ok = wait.go(kGFull, k & 1))) break;
             load_bc(&c_map, base + kOffC, k + 1);
             cs = k + 2;
@@ -814,6 +845,7 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
                 if (k + 2 < K) load_x(k + 2);
             }
         }
+        if (K == 1) after_states();
         if (ok && K > 0 && g.len >= K * kQ && wait.go(kYStore0 + ((K - 1) & 1), (uint32_t)((K - 1) >> 1) & 1u))
             store_y(K - 1);
         if (lane == 0) {   // loads in flight must land
@@ -839,6 +871,7 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
                     const uint32_t off = ((uint32_t)(i >> 2) * kAtom + (uint32_t)(i & 3) * 32u) >> 4;
                     mma_bf16(tmem + kColG, dc + off, db + off, id_g, i > 0);
                 }
+                if (k == 0) after_states();
                 wait.one(kHReady, k & 1);
                 if (k > 0) wait.one(kYFree, (k - 1) & 1);
                 tc_after_sync();
@@ -900,6 +933,7 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
                                 : g.seg > 0 ? seg_state(p, place - 1, h)
                                             : (resumed ? seg_state(p, g.base + g.nseg - 1, h) : nullptr);
             float v[32];
+            after_states();
             load_state(from, r, hq, v);
             if (K > 0) {
                 start(v, ex2(step[head].s[kQ - 1]));
@@ -1135,20 +1169,18 @@ cudaError_t launch_ssd_packed(const SsdPackedParams &p, cudaStream_t stream)
     if (e == cudaSuccess && p.seg_chunks)
         e = cudaFuncSetAttribute(ssd_packed_states_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)kStSmemBytes);
-    if (e == cudaSuccess) e = cudaMemsetAsync(p.status, 0, sizeof(int), stream);
     if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(ssd_packed_places(p.tokens, p.nseq, p.seg_chunks) *
-                                                pairs_of(p.nheads, p.ngroups));
-    if (p.seg_chunks) {
-        ssd_packed_states_kernel<<<grid, kThreads, kStSmemBytes, stream>>>(xm, bm, p);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-        ssd_packed_pass_kernel<<<static_cast<unsigned>(p.nseq * p.nheads * (kP * kN / 4 / 256)), 256, 0, stream>>>(p);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(ssd_packed_places(p.tokens, p.nseq, p.seg_chunks) *
+                                          pairs_of(p.nheads, p.ngroups)));
+    ssd_packed_clear_kernel<<<1, 1, 0, stream>>>(p.status);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && p.seg_chunks) {
+        e = launch_dependent(ssd_packed_states_kernel, grid, kThreads, kStSmemBytes, stream, xm, bm, p);
+        if (e == cudaSuccess)
+            e = launch_dependent(ssd_packed_pass_kernel,
+                                 dim3(static_cast<unsigned>(p.nseq * p.nheads * (kP * kN / 4 / 256))), 256, 0, stream, p);
     }
-    kernel<<<grid, kThreads, kSmemBytes, stream>>>(xm, bm, cm, ym, p);
-    return cudaGetLastError();
+    return e == cudaSuccess ? launch_dependent(kernel, grid, kThreads, kSmemBytes, stream, xm, bm, cm, ym, p) : e;
 }
 
 }  // namespace ms

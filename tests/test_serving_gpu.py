@@ -430,6 +430,16 @@ def test_norm_bwd(ms, rows, dim, group, dtype, residual, gate, first, weight, la
         assert got[key[k]] is None
 
 
+@pytest.mark.parametrize("rows,dim,group,dtype,residual,gate,first", [
+    (9001, 512, 512, "bf16", None, True, True), (2500, 1530, 1530, "f32", "f32", False, True),
+    (750, 16384, 16384, "bf16", None, True, False), (1999, 2048, 2048, "bf16", "f32", False, True),
+    (20011, 48, 16, "bf16", "bf16", False, True), (1200, 4096, 4096, "f32", None, False, True),
+])
+def test_norm_bwd_many_rows(ms, rows, dim, group, dtype, residual, gate, first):
+    """More rows than a team of threads has on their way together."""
+    test_norm_bwd(ms, rows, dim, group, dtype, residual, gate, first, True, residual is not None)
+
+
 def test_norm_bwd_against_differences(ms):
     """The gradients of x, z and weight against central differences of the forward in 64 bits."""
     g = rng(77)
