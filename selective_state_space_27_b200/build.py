@@ -1,4 +1,5 @@
-"""Build the sm_100a CUDA library ``libmambascan.so`` in-tree with nvcc.
+"""Build the sm_100a CUDA library ``libmambascan.so`` in-tree with nvcc, and the
+Python calls' tensor checks ``_binding.so`` with the host compiler.
 
 Usage: ``python -m selective_state_space_27_b200.build`` (or ``build()``).
 The library links the CUDA runtime statically, so it only needs the driver.
@@ -9,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmambascan.so")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["api.cu", "scan_fwd.cu", "scan_rec.cu", "scan_bwd.cu", "state_update.cu", "noalloc.cu", "ssd_fwd.cu", "probe.cu",
            "conv_packed.cu", "ssd_update.cu", "norm.cu", "ssd_packed.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -36,10 +39,29 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile csrc/binding.cpp against torch's and Python's headers."""
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"]]
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-shared", "-fPIC", "-O2", "-std=c++17",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in include),
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -61,8 +83,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         subprocess.check_call(cmd)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as pool:
+    with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 1)) as pool:
+        binding = pool.submit(build_binding, verbose)
         objs = list(pool.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     if verbose:

@@ -1,10 +1,11 @@
 """Mamba-2 serving operators and norms: packed sequences, states in cache slots.
 
 The calls that a serving step makes for every layer: on small batches they are
-bound by the host, so this module marshals lean. Arguments are checked once and
-packed into the C structs of ``include/mambascan.h`` with :mod:`struct`; the
-structs' ctypes mirrors (``ConvPackedArgs`` and so on) describe the same
-layouts. Outputs are allocated here unless ``out`` is given.
+bound by the host, so this module marshals lean. Tensors are checked once, by the
+compiled ``_binding`` (``csrc/binding.cpp``), and their pointers and strides packed
+into the C structs of ``include/mambascan.h`` with :mod:`struct`; the structs'
+ctypes mirrors (``ConvPackedArgs`` and so on) describe the same layouts. Outputs
+are allocated here unless ``out`` is given.
 """
 from __future__ import annotations
 
@@ -15,6 +16,12 @@ import torch
 
 from . import (MS_BF16, MS_F32, SSD_DSTATE, SSD_HEADDIM, MambaScanError, load_library, ssd_check)
 
+try:
+    from ._binding import empty_like as _empty_like, rows as _rows, scratch as _scratch, vector as _vector
+except ImportError as e:
+    raise RuntimeError("the compiled tensor checks are not built or do not fit this torch "
+                       "(run python -m selective_state_space_27_b200.build)") from e
+
 # struct layouts, field by field as in the header (P: pointer, q: int64, i: int32, f: float, B: uint8)
 CONV_PACKED = struct.Struct("@4q2i Pq Pq Pqq PPP")
 CONV1D = struct.Struct("@PPii")
@@ -23,8 +30,10 @@ SSD_UPDATE = struct.Struct("@6q2i Pq Pq Pq Pq Pq Pq Pq PPPP")
 NORM = struct.Struct("@3q2i2f2i Pq Pq Pq Pq Pq P")
 NORM_BWD = struct.Struct("@Pq Pq Pq Pq Pq P")
 
+_F32 = torch.float32
 _DTYPES = {torch.float32: MS_F32, torch.bfloat16: MS_BF16}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _fns = {}
 
 
@@ -44,7 +53,7 @@ _str, _ptr, _size = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t
 
 def _run(device, stream, fn, *args):
     """``fn(*args, stream)`` with ``device`` current, on ``stream`` or the device's current stream."""
-    if device.index != torch.cuda.current_device():
+    if device.index != _current_device():
         with torch.cuda.device(device):
             return _run(device, stream, fn, *args)
     if stream is not None:
@@ -60,7 +69,7 @@ def _run(device, stream, fn, *args):
 
 def _workspace_bytes(device, name, args):
     """Bytes that a workspace query reports for the packed ``args`` on ``device``."""
-    if device.index != torch.cuda.current_device():
+    if device.index != _current_device():
         with torch.cuda.device(device):
             return _workspace_bytes(device, name, args)
     n = _size(0)
@@ -70,14 +79,15 @@ def _workspace_bytes(device, name, args):
     return n.value
 
 
-def _workspace(device, workspace, need):
-    """(tensor, whether it was allocated here) of at least ``need`` bytes."""
+def _workspace(x, workspace, need):
+    """(tensor on x's device, whether it was allocated here) of at least ``need`` bytes."""
     if workspace is not None:
+        device = x.device
         if workspace.dtype is not torch.uint8 or workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
         if workspace.numel() >= need:
             return workspace, False
-    return torch.empty(need, dtype=torch.uint8, device=device), True
+    return _scratch(need, x), True
 
 
 def _keep(t, stream):
@@ -96,43 +106,6 @@ def _cuda(x, ndim, what):
     if code is None:
         raise TypeError(f"unsupported dtype {x.dtype} (float32 or bfloat16)")
     return x.device, code
-
-
-def _refuse(name, t, dtype, shape, device):
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _rows(name, t, dtype, shape, device):
-    """(pointer, stride of the first axis) of a tensor whose axes behind the first are contiguous."""
-    if t is None:
-        return 0, 0
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
-        _refuse(name, t, dtype, shape, device)
-    stride = t.stride()
-    if shape[0] <= 1 or not t.is_contiguous():
-        inner = 1
-        for n, st in zip(reversed(shape[1:]), reversed(stride[1:])):
-            if n > 1 and st != inner:
-                raise ValueError(f"{name} must be contiguous behind its first axis")
-            inner *= n
-        if shape[0] <= 1:
-            return t.data_ptr(), inner
-    return t.data_ptr(), stride[0]
-
-
-def _vector(name, t, n, device, dtype=torch.float32):
-    """Pointer of a contiguous vector of n values (0 for None)."""
-    if t is None:
-        return 0
-    if t.shape != (n,) or t.dtype is not dtype or t.device != device:
-        _refuse(name, t, dtype, (n,), device)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
 
 
 def _slots(nseq, state_indices, has_initial_state, device):
@@ -157,20 +130,19 @@ def _offsets(cu_seqlens, device):
 def _conv(x, weight, bias, silu, cu, nseq, state, state_indices, has_initial_state, out, stream):
     device, code = _cuda(x, 2, "x")
     tokens, channels = shape = x.shape
-    y = x.new_empty(shape) if out is None else out
+    y = _empty_like(x) if out is None else out
     if weight.dim() != 2:
         raise ValueError("conv weight must be (channels, width)")
     width = weight.shape[1]
-    if weight.shape[0] != channels or not weight.is_contiguous():
+    wp, ws = _rows("conv weight", weight, torch.float32, (channels, width), device)
+    if ws != width:
         raise ValueError("conv weight must be contiguous with one row per channel")
-    if weight.dtype is not torch.float32 or weight.device != device:
-        _refuse("conv weight", weight, torch.float32, (channels, width), device)
     idx, flags = _slots(nseq, state_indices, has_initial_state, device)
     st = slot_stride = row_stride = slots = 0
     if state is not None:
         slots = state.shape[0] if state.dim() == 3 else -1
         if state.shape != (slots, width - 1, channels) or state.dtype is not x.dtype or state.device != device:
-            _refuse("state", state, x.dtype, ("slots", width - 1, channels), device)
+            _rows("state", state, x.dtype, ("slots", width - 1, channels), device)   # (raises)
         slot_stride, row_stride, last = state.stride()
         if last != 1 and channels > 1:
             raise ValueError("state must be contiguous along the channels")
@@ -181,7 +153,7 @@ def _conv(x, weight, bias, silu, cu, nseq, state, state_indices, has_initial_sta
     yp, ys = _rows("out", y, x.dtype, shape, device)
     args = CONV_PACKED.pack(tokens, channels, nseq, slots, code, 0, xp, xs, yp, ys, st, slot_stride, row_stride,
                             cu, idx, flags)
-    conv = CONV1D.pack(weight.data_ptr(), _vector("conv bias", bias, channels, device), width, 1 if silu else 0)
+    conv = CONV1D.pack(wp, _vector("conv bias", bias, channels, device, _F32), width, 1 if silu else 0)
     _run(device, stream, _fn("mamba_conv_packed_fwd", _str, _str, _ptr), args, conv)
     return y
 
@@ -219,8 +191,8 @@ def _ssd_state(state, nheads, headdim, dstate, device):
     """(slots, pointer, slot stride) of a cache of float32 states."""
     slots = state.shape[0] if state.dim() == 4 else -1
     shape = (slots, nheads, headdim, dstate)
-    if state.shape != shape or state.dtype is not torch.float32 or state.device != device:
-        _refuse("state", state, torch.float32, ("slots", nheads, headdim, dstate), device)
+    if slots < 0:
+        shape = ("slots", nheads, headdim, dstate)
     ptr, stride = _rows("state", state, torch.float32, shape, device)
     return slots, ptr, stride
 
@@ -252,7 +224,7 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
     cu, nseq = _offsets(cu_seqlens, device)
     if B.dim() != 3:
         raise ValueError(f"B must be (tokens, ngroups, {SSD_DSTATE})")
-    y = x.new_empty(shape) if out is None else out
+    y = _empty_like(x) if out is None else out
     bc = (tokens, B.shape[1], SSD_DSTATE)
     idx, flags = _slots(nseq, state_indices, has_initial_state, device)
     slots, st, slot_stride = (0, 0, 0) if state is None else _ssd_state(state, nheads, headdim, SSD_DSTATE, device)
@@ -260,10 +232,10 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
         tokens, nseq, nheads, bc[1], slots, int(max_seqlen), code, 1 if dt_softplus else 0,
         *_rows("x", x, dtype, shape, device), *_rows("dt", dt, dtype, (tokens, nheads), device),
         *_rows("B", B, dtype, bc, device), *_rows("C", C, dtype, bc, device), *_rows("z", z, dtype, shape, device),
-        *_rows("out", y, dtype, shape, device), _vector("A", A, nheads, device), _vector("D", D, nheads, device),
-        _vector("dt_bias", dt_bias, nheads, device), st, slot_stride, cu, idx, flags, int(wait_limit_us), 0)
+        *_rows("out", y, dtype, shape, device), _vector("A", A, nheads, device, _F32), _vector("D", D, nheads, device, _F32),
+        _vector("dt_bias", dt_bias, nheads, device, _F32), st, slot_stride, cu, idx, flags, int(wait_limit_us), 0)
     need = _workspace_bytes(device, "mamba_ssd_packed_workspace_size", args)
-    workspace, own = _workspace(device, workspace, need)
+    workspace, own = _workspace(x, workspace, need)
     _run(device, stream, _fn("mamba_ssd_packed_fwd", _str, _ptr, _size, _ptr), args, workspace.data_ptr(),
          workspace.numel())
     if own:
@@ -290,15 +262,15 @@ def ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_sof
     batch, nheads, headdim = shape = x.shape
     if B.dim() != 3:
         raise ValueError("B must be (batch, ngroups, dstate)")
-    y = x.new_empty(shape) if out is None else out
+    y = _empty_like(x) if out is None else out
     bc = (batch, B.shape[1], B.shape[2])
     slots, st, slot_stride = _ssd_state(state, nheads, headdim, bc[2], device)
     args = SSD_UPDATE.pack(
         batch, nheads, bc[1], headdim, bc[2], slots, code, 1 if dt_softplus else 0, st, slot_stride,
         *_rows("x", x, dtype, shape, device), *_rows("dt", dt, dtype, (batch, nheads), device),
         *_rows("B", B, dtype, bc, device), *_rows("C", C, dtype, bc, device), *_rows("z", z, dtype, shape, device),
-        *_rows("out", y, dtype, shape, device), _vector("A", A, nheads, device), _vector("D", D, nheads, device),
-        _vector("dt_bias", dt_bias, nheads, device), _vector("state_indices", state_indices, batch, device, torch.int32))
+        *_rows("out", y, dtype, shape, device), _vector("A", A, nheads, device, _F32), _vector("D", D, nheads, device, _F32),
+        _vector("dt_bias", dt_bias, nheads, device, _F32), _vector("state_indices", state_indices, batch, device, torch.int32))
     _run(device, stream, _fn("mamba_ssd_state_update", _str, _ptr), args)
     return y
 
@@ -325,12 +297,12 @@ def norm_fwd(x, weight=None, z=None, residual=None, residual_scale=1.0, eps=1e-5
     device, code = _cuda(x, 2, "x")
     dtype = x.dtype
     rows, dim = shape = x.shape
-    y = x.new_empty(shape) if out is None else out
+    y = _empty_like(x) if out is None else out
     res_code, res, ro = code, (0, 0), (0, 0)
     if residual is not None:
         res_code = _residual_code(residual, dtype)
         if residual_out is None:
-            residual_out = residual.new_empty(shape)
+            residual_out = _empty_like(residual)
         res = _rows("residual", residual, residual.dtype, shape, device)
         ro = _rows("residual_out", residual_out, residual.dtype, shape, device)
     elif residual_out is not None:
@@ -338,7 +310,7 @@ def norm_fwd(x, weight=None, z=None, residual=None, residual_scale=1.0, eps=1e-5
     args = NORM.pack(rows, dim, dim if group_size is None else group_size, code, res_code, eps, residual_scale,
                      1 if gate_first else 0, 0, *_rows("x", x, dtype, shape, device),
                      *_rows("z", z, dtype, shape, device), *res, *ro, *_rows("out", y, dtype, shape, device),
-                     _vector("weight", weight, dim, device))
+                     _vector("weight", weight, dim, device, _F32))
     _run(device, stream, _fn("mamba_norm_fwd", _str, _ptr), args)
     return y, residual_out
 
@@ -356,18 +328,18 @@ def norm_bwd(dy, x, weight=None, z=None, residual_out=None, dresidual_out=None, 
     device, code = _cuda(x, 2, "x")
     dtype = x.dtype
     rows, dim = shape = x.shape
-    out = {"dx": x.new_empty(shape), "dz": None, "dresidual": None, "dweight": None}
+    out = {"dx": _empty_like(x), "dz": None, "dresidual": None, "dweight": None}
     res_code, ro, dro, dres, dz = code, (0, 0), (0, 0), (0, 0), (0, 0)
     if residual_out is not None:
         res_code = _residual_code(residual_out, dtype)
         ro = _rows("residual_out", residual_out, residual_out.dtype, shape, device)
         dro = _rows("dresidual_out", dresidual_out, residual_out.dtype, shape, device)
-        out["dresidual"] = residual_out.new_empty(shape)
+        out["dresidual"] = _empty_like(residual_out)
         dres = out["dresidual"].data_ptr(), dim
     elif dresidual_out is not None:
         raise ValueError("dresidual_out needs residual_out")
     if z is not None:
-        out["dz"] = x.new_empty(shape)
+        out["dz"] = _empty_like(x)
         dz = out["dz"].data_ptr(), dim
     dw = 0
     if weight is not None:
@@ -375,13 +347,13 @@ def norm_bwd(dy, x, weight=None, z=None, residual_out=None, dresidual_out=None, 
         dw = out["dweight"].data_ptr()
     args = NORM.pack(rows, dim, dim if group_size is None else group_size, code, res_code, eps, residual_scale,
                      1 if gate_first else 0, 0, *_rows("x", x, dtype, shape, device),
-                     *_rows("z", z, dtype, shape, device), 0, 0, *ro, 0, 0, _vector("weight", weight, dim, device))
+                     *_rows("z", z, dtype, shape, device), 0, 0, *ro, 0, 0, _vector("weight", weight, dim, device, _F32))
     grads = NORM_BWD.pack(*_rows("dy", dy, dtype, shape, device), *dro, out["dx"].data_ptr(), dim, *dz, *dres, dw)
     ws, own = None, False
     if dw:
         need = _workspace_bytes(device, "mamba_norm_bwd_workspace_size", args)
         if need:
-            ws, own = _workspace(device, workspace, need)
+            ws, own = _workspace(x, workspace, need)
     _run(device, stream, _fn("mamba_norm_bwd", _str, _str, _ptr, _size, _ptr), args, grads,
          0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     if own:

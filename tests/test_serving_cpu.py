@@ -10,7 +10,9 @@ import torch
 
 import selective_state_space_27_b200 as ms
 from selective_state_space_27_b200 import build as msbuild
-from selective_state_space_27_b200 import serving
+
+msbuild.build()
+from selective_state_space_27_b200 import serving   # noqa: E402  (needs the compiled tensor checks)
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 INCLUDE = os.path.join(ROOT, "include")
@@ -220,6 +222,44 @@ def test_python_calls_refuse_host_tensors():
         ms.ssd_state_update(f(2, 1, 4, 8), f(2, 1, 4), f(2, 1), f(1), f(2, 1, 8), f(2, 1, 8))
     with pytest.raises(AttributeError):
         ms.no_such_name
+
+
+def test_tensor_checks():
+    """The compiled checks: pointers, strides and refusals."""
+    from selective_state_space_27_b200 import _binding as b
+    f32, cpu = torch.float32, torch.device("cpu")
+    x = torch.zeros(6, 4, 8)
+    assert b.rows("x", x, f32, x.shape, cpu) == (x.data_ptr(), 32)
+    y = torch.zeros(6, 50)[:, 10:42].unflatten(1, (4, 8))
+    assert b.rows("y", y, f32, (6, 4, 8), cpu) == (y.data_ptr(), 50)
+    assert b.rows("x", x[:1], f32, (1, 4, 8), cpu) == (x.data_ptr(), 32)
+    assert b.rows("x", x[:0], f32, (0, 4, 8), cpu)[1] == 32
+    assert b.rows("x", x[:1].expand(6, 4, 8), f32, (6, 4, 8), cpu) == (x.data_ptr(), 0)
+    assert b.rows("none", None, f32, (1,), cpu) == (0, 0) and b.vector("none", None, 3, cpu, f32) == 0
+    for bad in (x.transpose(1, 2).contiguous().transpose(1, 2), x[:, :, ::2], x.expand(6, 4, 8)[:, ::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            b.rows("x", bad, f32, bad.shape, cpu)
+    with pytest.raises(TypeError, match="x must be torch.bfloat16, got torch.float32"):
+        b.rows("x", x, torch.bfloat16, x.shape, cpu)
+    with pytest.raises(ValueError, match="shape"):
+        b.rows("x", x, f32, (6, 4, 9), cpu)
+    with pytest.raises(ValueError, match="slots"):
+        b.rows("x", x, f32, ("slots", 4, 8), cpu)
+    with pytest.raises(ValueError, match="is on cpu"):
+        b.rows("x", x, f32, x.shape, torch.device("cuda", 0))
+    with pytest.raises(TypeError, match="tensor"):
+        b.rows("x", [1.0], f32, (1,), cpu)
+    v = torch.arange(5, dtype=torch.int32)
+    assert b.vector("v", v, 5, cpu, torch.int32) == v.data_ptr()
+    with pytest.raises(ValueError, match="shape"):
+        b.vector("v", v, 4, cpu, torch.int32)
+    with pytest.raises(ValueError, match="contiguous"):
+        b.vector("v", torch.zeros(10)[::2], 5, cpu, f32)
+    with pytest.raises(TypeError):
+        b.vector("v", v, 5, cpu, f32)
+    e = b.empty_like(y)
+    assert e.shape == y.shape and e.dtype is f32 and e.is_contiguous()
+    assert b.scratch(300, x).shape == (300,) and b.scratch(0, x).dtype is torch.uint8
 
 
 def test_segments_have_places():
