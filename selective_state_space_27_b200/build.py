@@ -32,17 +32,22 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "binding.cpp"]
     files.append(os.path.join(INCLUDE, "mambascan.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _newer(LIB, _inputs())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING, [os.path.join(CSRC, "binding.cpp"), os.path.abspath(__file__)])
+
+
+def _newer(target, files) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target) for f in files)
 
 
 def build_binding(verbose: bool = False) -> str:
@@ -65,7 +70,9 @@ def build_binding(verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every CUDA source for sm_100a into the in-tree shared library."""
+    """Compile every CUDA source for sm_100a into the in-tree shared library, and the binding."""
+    if force or not binding_up_to_date():
+        build_binding(verbose)
     if not force and up_to_date():
         return LIB
     objdir = os.path.join(PKG, "_build")
@@ -83,10 +90,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         subprocess.check_call(cmd)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 1)) as pool:
-        binding = pool.submit(build_binding, verbose)
+    with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as pool:
         objs = list(pool.map(compile_one, SOURCES))
-        binding.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     if verbose:
