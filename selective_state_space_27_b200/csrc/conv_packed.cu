@@ -8,14 +8,15 @@
 // float32 operations per element: bound by HBM bandwidth. A thread owns four
 // channels and slides a window of W inputs down the tokens in registers, so an
 // input is loaded once per tile of tokens plus W - 1 look-back rows per tile.
-// Measured on B200 for 24000 tokens x 4352 channels, bf16, W = 4: 85 us (75% of
-// the measured copy bandwidth); 89 us with blocks of 256 threads instead of 64
-// (28 warps per SM fit instead of 32), 117 us with eight channels per thread (too
-// few warps), 89 us with two (1280 threads per SM, twice the rows in flight),
-// 104 us with eight tiles per thread instead of one stretch of rows, 104 and 135 us
-// with two and eight rows loaded ahead instead of four. The special function unit
-// is 59% busy (exponential and reciprocal of the SiLU); the rest is the latency
-// of loads at the 64 registers per thread that 32 warps leave.
+// Measured on B200 for 24000 tokens x 4352 channels, bf16, W = 4: 83 us (77% of
+// the measured copy bandwidth). The next rows of a thread wait in shared memory
+// (with the next four in registers 85 us). Four rows at a time, three times: 84
+// us with two times or with two rows, 88 us with eight rows twice; 88 us with 1280
+// threads per SM (48 registers: spills), 89 us with blocks of 256 threads instead
+// of 64 (28 warps per SM fit instead of 32). Measured before the rows waited in
+// shared memory: eight channels per thread 117 us (too few warps), two 89 us,
+// eight tiles per thread instead of one stretch of rows 104 us. The special
+// function unit is 59% busy (exponential and reciprocal of the SiLU).
 //
 // Two kinds of work. A tile is a stretch of consecutive rows of the packed
 // stream, whatever sequences they belong to, except each sequence's first
@@ -30,6 +31,7 @@
 namespace ms {
 namespace {
 
+constexpr int S = 3, U = 4;                // batches in shared memory, rows of a batch
 constexpr int kMaxThreads = 64;
 constexpr int kThreadsPerSm = 1024;        // threads that run together on an SM
 
@@ -149,10 +151,22 @@ __device__ __forceinline__ void sequence_start(const ConvPackedParams &p, const 
     }
 }
 
+// One value of the ring (8 or 16 bytes).
+template <typename R>
+__device__ __forceinline__ R load_ring(uint32_t at) {
+    union { R r; uint32_t w[sizeof(R) / 4]; } v;
+    if constexpr (sizeof(R) == 8)
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.w[0]), "=r"(v.w[1]) : "r"(at) : "memory");
+    else
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]) : "r"(at) : "memory");
+    return v.r;
+}
+
 // Rows [t0, t1) of the packed stream, without the first W - 1 of each sequence.
 template <typename T, int VEC, int W>
 __device__ __forceinline__ void tile_rows(const ConvPackedParams &p, const Taps<T, VEC, W> &f, int t0, int t1,
-                                          int64_t c, bool on) {
+                                          int64_t c, bool on, uint32_t ring) {
     const T *x = static_cast<const T *>(p.x) + c;
     T *y = static_cast<T *>(p.y) + c;
     const int nseq = static_cast<int>(p.nseq);
@@ -170,29 +184,39 @@ __device__ __forceinline__ void tile_rows(const ConvPackedParams &p, const Taps<
 #pragma unroll
         for (int j = 0; j + 1 < W; ++j)
             widen<T, VEC>(load_raw<T, VEC>(x + (from - (W - 1) + static_cast<int64_t>(j)) * p.x_st), win[j + 1]);
-        constexpr int U = 4;   // loads in flight per thread
         const T *xp = x + from * p.x_st;
         T *yp = y + from * p.y_st;
-        if (from + U <= to) {
-            // the next U rows are loaded while this thread works on U
-            Raw<T, VEC> r[U];
+        constexpr int B = sizeof(Raw<T, VEC>);
+        if constexpr (B >= 8) {
+            // batches of U rows on their way in shared memory (each thread its own values)
+            const int batches = (to - from) / U;
+            auto place = [&](int b, int u) {
+                return ring + (static_cast<uint32_t>(b % S * U + u) * blockDim.x + threadIdx.x) * B;
+            };
+            const T *ahead = xp;
+            auto issue = [&](int b) {
+                if (b < batches) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) r[u] = load_raw<T, VEC>(xp + u * p.x_st);
-            for (; from + U <= to; from += U) {
-                Raw<T, VEC> n[U];
-                xp += U * p.x_st;
-                const bool more = from + 2 * U <= to;
+                    for (int u = 0; u < U; ++u) cp_async_full<B>(place(b, u), ahead + u * p.x_st);
+                    ahead += U * p.x_st;
+                }
+                cp_async_commit();
+            };
 #pragma unroll
-                for (int u = 0; u < U; ++u) n[u] = more ? load_raw<T, VEC>(xp + u * p.x_st) : r[u];
+            for (int b = 0; b + 1 < S; ++b) issue(b);
+            for (int b = 0; b < batches; ++b) {
+                issue(b + S - 1);
+                cp_async_wait<S - 1>();
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     shift<W, VEC>(win);
-                    widen<T, VEC>(r[u], win[W - 1]);
+                    widen<T, VEC>(load_ring<Raw<T, VEC>>(place(b, u)), win[W - 1]);
                     store_raw<T, VEC>(yp + u * p.y_st, f.apply(win));
-                    r[u] = n[u];
                 }
                 yp += U * p.y_st;
             }
+            from += batches * U;
+            xp += static_cast<int64_t>(batches) * U * p.x_st;
         }
         for (; from < to; ++from) {
             shift<W, VEC>(win);
@@ -208,6 +232,8 @@ __device__ __forceinline__ void tile_rows(const ConvPackedParams &p, const Taps<
 // tiles blockIdx.x, blockIdx.x + gridDim.x, ...
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kMaxThreads, kThreadsPerSm / kMaxThreads) conv_packed_kernel(const ConvPackedParams p) {
+    extern __shared__ __align__(16) uint8_t rows_ahead[];
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(rows_ahead));
     const int64_t c = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * VEC;
     const bool on = c < p.channels;
     Taps<T, VEC, W> f;
@@ -217,7 +243,7 @@ __global__ void __launch_bounds__(kMaxThreads, kThreadsPerSm / kMaxThreads) conv
     const int64_t skip = p.nseq % gridDim.x, b = blockIdx.x;
     for (int64_t i = b >= skip ? b - skip : b + gridDim.x - skip; i < p.tiles; i += gridDim.x)
         tile_rows<T, VEC, W>(p, f, static_cast<int>(i * p.tile), static_cast<int>(min64((i + 1) * p.tile, p.tokens)), c,
-                             on);
+                             on, ring);
 }
 
 template <typename T, int VEC>
@@ -234,11 +260,12 @@ cudaError_t launch_w(const ConvPackedParams &p0, int num_sms, cudaStream_t strea
     p.tiles = p.cu ? (p.tokens + p.tile - 1) / p.tile : 0;
     p.w_vec = reinterpret_cast<uintptr_t>(p.weight) % 16 == 0;
     const dim3 grid(static_cast<unsigned>(min64(p.nseq + p.tiles, most)), static_cast<unsigned>(nb));
+    const size_t smem = p.tiles && sizeof(Raw<T, VEC>) >= 8 ? sizeof(Raw<T, VEC>) * S * U * threads : 0;
     switch (p.width) {
-    case 1: conv_packed_kernel<T, VEC, 1><<<grid, threads, 0, stream>>>(p); break;
-    case 2: conv_packed_kernel<T, VEC, 2><<<grid, threads, 0, stream>>>(p); break;
-    case 3: conv_packed_kernel<T, VEC, 3><<<grid, threads, 0, stream>>>(p); break;
-    default: conv_packed_kernel<T, VEC, 4><<<grid, threads, 0, stream>>>(p); break;
+    case 1: conv_packed_kernel<T, VEC, 1><<<grid, threads, smem, stream>>>(p); break;
+    case 2: conv_packed_kernel<T, VEC, 2><<<grid, threads, smem, stream>>>(p); break;
+    case 3: conv_packed_kernel<T, VEC, 3><<<grid, threads, smem, stream>>>(p); break;
+    default: conv_packed_kernel<T, VEC, 4><<<grid, threads, smem, stream>>>(p); break;
     }
     return cudaGetLastError();
 }

@@ -35,13 +35,18 @@ __device__ __forceinline__ int block_slot(const int32_t *idx, int64_t s, int64_t
     return __syncthreads_or(twin) || !in ? -1 : v;
 }
 
-// First sequence whose end lies behind token t (nseq if none does).
+// First sequence whose end lies behind token t (nseq if none does). Called by
+// whole warps, whose lanes look at 32 sequences in one round of loads.
 __device__ __forceinline__ int seq_of_token(const int32_t *cu, int nseq, int t) {
-    int lo = 0, hi = nseq;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(cu + mid + 1) > t) hi = mid;
-        else lo = mid + 1;
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    for (int n = nseq; n > 0;) {
+        const int step = (n + 31) / 32, c = lane * step;
+        const bool ended = c < n && __ldg(cu + lo + c + 1) <= t;
+        const int k = __popc(__ballot_sync(0xffffffffu, ended));   // (the first k probes, the offsets never fall)
+        if (k == 0) break;
+        lo += (k - 1) * step + 1;
+        n = min(step - 1, n - (k - 1) * step - 1);
     }
     return lo;
 }
