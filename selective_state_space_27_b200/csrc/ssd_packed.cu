@@ -55,7 +55,8 @@
 // warps' own accesses (1800), so that arithmetic beside the products slows both.
 // Measured and not kept (4 x 8192 x 64 heads, against 240 us): C H^T issued before
 // G 259 us; w X made while M' X runs 249 us; X kept in registers 241 us (spills);
-// one head per CTA and two CTAs per SM 298 us; w X shared out unevenly 271 us.
+// one head per CTA and two CTAs per SM 298 us; w X shared out unevenly 271 us; M'
+// made while C H^T runs and the next hi term beside M' X (X then read twice) 255 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
