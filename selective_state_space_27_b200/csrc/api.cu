@@ -883,11 +883,11 @@ static ms_status check_ssd_packed(const ms_ssd_packed_args *a) {
     return MS_OK;
 }
 
-static ms_status ssd_packed_segment(const ms_ssd_packed_args *a, int *chunks) {
+static ms_status ssd_packed_plan(const ms_ssd_packed_args *a, ms::SsdPackedPlan *plan) {
     int sms = 0;
     const ms_status st = device_sms(&sms);
     if (st != MS_OK) return st;
-    *chunks = ms::ssd_packed_segment(a->tokens, a->nseq, a->nheads, a->ngroups, a->max_seqlen, sms);
+    *plan = ms::ssd_packed_plan(a->tokens, a->nseq, a->nheads, a->ngroups, a->max_seqlen, sms);
     return MS_OK;
 }
 
@@ -896,10 +896,10 @@ ms_status mamba_ssd_packed_workspace_size(const ms_ssd_packed_args *a, size_t *b
     *bytes = 0;
     ms_status st = check_ssd_packed(a);
     if (st != MS_OK) return st;
-    int chunks = 0;
-    st = ssd_packed_segment(a, &chunks);
+    ms::SsdPackedPlan plan{};
+    st = ssd_packed_plan(a, &plan);
     if (st != MS_OK) return st;
-    *bytes = ms::ssd_packed_ws_bytes(a->tokens, a->nseq, a->nheads, chunks);
+    *bytes = ms::ssd_packed_ws_bytes(a->tokens, a->nseq, a->nheads, plan.seg_chunks);
     return MS_OK;
 }
 
@@ -907,10 +907,10 @@ ms_status mamba_ssd_packed_fwd(const ms_ssd_packed_args *a, void *workspace, siz
     const CallRange range("mamba_ssd_packed_fwd");
     ms_status st = check_ssd_packed(a);
     if (st != MS_OK) return st;
-    int chunks = 0;
-    st = ssd_packed_segment(a, &chunks);
+    ms::SsdPackedPlan plan{};
+    st = ssd_packed_plan(a, &plan);
     if (st != MS_OK) return st;
-    const size_t need = ms::ssd_packed_ws_bytes(a->tokens, a->nseq, a->nheads, chunks);
+    const size_t need = ms::ssd_packed_ws_bytes(a->tokens, a->nseq, a->nheads, plan.seg_chunks);
     if (!workspace || workspace_bytes < need) {
         set_error("workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : static_cast<size_t>(0));
         return MS_ERR_WORKSPACE;
@@ -934,7 +934,7 @@ ms_status mamba_ssd_packed_fwd(const ms_ssd_packed_args *a, void *workspace, siz
     p.cu = a->cu_seqlens; p.idx = a->state_indices; p.has_init = a->has_initial_state;
     p.softplus = a->dt_softplus ? 1 : 0;
     p.wait_limit_ns = a->wait_limit_us ? 1000ull * a->wait_limit_us : 1000000000ull;
-    p.seg_chunks = chunks;
+    p.seg_chunks = plan.seg_chunks; p.each = plan.each;
     ms::ssd_packed_bind(p, workspace);
     const cudaError_t e = ms::launch_ssd_packed(p, s);
     if (e == cudaErrorNotSupported) return unsupported("the driver offers no tensor-map encoder");

@@ -284,11 +284,15 @@ struct SsdPackedParams {
     // Sequences are cut into segments of seg_chunks chunks of 128 tokens (0:
     // not cut). seg_states: (segment places, nheads, 64, 128) zero-start end
     // states, seg_decay: (segment places, nheads) their decays (log2).
-    int seg_chunks;
+    int seg_chunks, each;     // each: heads per CTA, 1 or 2
     float *seg_states, *seg_decay;
 };
-// Chunks per segment for these sizes (0: sequences are not cut).
-int ssd_packed_segment(int64_t tokens, int64_t nseq, int64_t nheads, int64_t ngroups, int64_t max_seqlen, int num_sms);
+// Chunks per segment (0: sequences are not cut) and heads per CTA for these sizes.
+struct SsdPackedPlan {
+    int seg_chunks, each;
+};
+SsdPackedPlan ssd_packed_plan(int64_t tokens, int64_t nseq, int64_t nheads, int64_t ngroups, int64_t max_seqlen,
+                              int num_sms);
 // Places for segments: at least the number of segments of any split of tokens into nseq sequences.
 int64_t ssd_packed_places(int64_t tokens, int64_t nseq, int seg_chunks);
 size_t ssd_packed_ws_bytes(int64_t tokens, int64_t nseq, int64_t nheads, int seg_chunks);

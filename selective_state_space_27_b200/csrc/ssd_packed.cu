@@ -401,20 +401,21 @@ __device__ __forceinline__ float *seg_state(const SsdPackedParams &p, int64_t pl
     return p.seg_states + (place * p.nheads + h) * (int64_t)(kP * kN);
 }
 
-// Heads h and (nh == 2) h + 1 of group `group`.
+// Heads h and (nh == 2) h + 1 of group `group`: up to `each` heads of a group per CTA.
 struct Pair {
     int h, nh, group;
 };
 
-__host__ __device__ __forceinline__ int64_t pairs_of(int64_t nheads, int64_t ngroups)
+__host__ __device__ __forceinline__ int64_t pairs_of(int64_t nheads, int64_t ngroups, int each)
 {
-    return ngroups * ((nheads / ngroups + 1) / 2);
+    return ngroups * ((nheads / ngroups + each - 1) / each);
 }
 
 __device__ __forceinline__ Pair pair_of(const SsdPackedParams &p, int i)
 {
-    const int hpg = (int)(p.nheads / p.ngroups), ppg = (hpg + 1) / 2, group = i / ppg, first = 2 * (i - group * ppg);
-    return {group * hpg + first, min(2, hpg - first), group};
+    const int hpg = (int)(p.nheads / p.ngroups), ppg = (hpg + p.each - 1) / p.each, group = i / ppg;
+    const int first = p.each * (i - group * ppg);
+    return {group * hpg + first, min(p.each, hpg - first), group};
 }
 
 // Set up by all threads: barriers, tensor memory, the segment; false when the
@@ -476,7 +477,7 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = smem_addr(smem);
-    const int pairs = (int)pairs_of(p.nheads, p.ngroups);
+    const int pairs = (int)pairs_of(p.nheads, p.ngroups, p.each);
     const int64_t place = blockIdx.x / pairs;
     const Pair hp = pair_of(p, (int)(blockIdx.x - place * pairs));
     Segment g;
@@ -740,7 +741,7 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = smem_addr(smem);
-    const int pairs = (int)pairs_of(p.nheads, p.ngroups);
+    const int pairs = (int)pairs_of(p.nheads, p.ngroups, p.each);
     const int64_t place = blockIdx.x / pairs;
     const Pair hp = pair_of(p, (int)(blockIdx.x - place * pairs));
     Segment g;
@@ -1094,34 +1095,45 @@ bool encode_rows(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, i
 
 }  // namespace
 
-// Chunks per segment (0: sequences are not cut): the smallest estimate of the
-// time, in chunk times of the num_sms CTAs that run together. n CTAs of at
+// A chunk of one head takes kOneHead of the time of a chunk of two.
+constexpr double kOneHead = 0.7;
+
+// Chunks per segment (0: sequences are not cut) and heads per CTA: the smallest
+// estimate of the time, in chunk times of the num_sms CTAs that run together. n CTAs of at
 // most c chunks take c when they all run at once, else their work spread over
 // the places plus half a CTA at the end. A CTA's start costs about 0.7 of a
 // chunk; a chunk of the first kernel costs half as much as one of the third,
 // and the additional launches and the pass along the segments about 1 and one
 // thousandth of a chunk for each segment and head.
-int ssd_packed_segment(int64_t tokens, int64_t nseq, int64_t nheads, int64_t ngroups, int64_t max_seqlen, int num_sms)
+SsdPackedPlan ssd_packed_plan(int64_t tokens, int64_t nseq, int64_t nheads, int64_t ngroups, int64_t max_seqlen, int num_sms)
 {
     const double slots = num_sms > 0 ? num_sms : 1;
     const int64_t longest = ((max_seqlen > 0 ? min64(max_seqlen, tokens) : tokens) + kQ - 1) / kQ;
-    const double chunks = (double)tokens / kQ + 0.5 * (double)nseq, h = (double)pairs_of(nheads, ngroups);
+    const double chunks = (double)tokens / kQ + 0.5 * (double)nseq;
     const auto spread = [&](double n, double mean, double most) {
         return n <= slots ? most : n * mean / slots + 0.5 * most;
     };
-    double best = spread((double)nseq * h, chunks / (double)nseq + 0.7, (double)longest + 0.7);
-    int pick = 0;
-    for (int c = 2; c < longest && c <= 128; ++c) {
-        const double segs = chunks / c + 0.5 * (double)nseq, mean = chunks / segs;
-        const double early = max64(0, (int64_t)(segs - (double)nseq));   // not their sequence's last
-        const double t = spread(segs * h, mean + 0.7, c + 0.7) + 0.5 * spread(early * h, c + 1.4, c + 1.4) + 1.0 +
-                         0.001 * early * h;
-        if (t < best) {
-            best = t;
-            pick = c;
+    SsdPackedPlan best{0, 2};
+    double least = 0;
+    for (int each = 2; each >= 1; --each) {
+        const double h = (double)pairs_of(nheads, ngroups, each), unit = each == 2 ? 1.0 : kOneHead;
+        const double whole = unit * spread((double)nseq * h, chunks / (double)nseq + 0.7, (double)longest + 0.7);
+        if (each == 2 || whole < least) {
+            least = whole;
+            best = {0, each};
+        }
+        for (int c = 2; c < longest && c <= 128; ++c) {
+            const double segs = chunks / c + 0.5 * (double)nseq, mean = chunks / segs;
+            const double early = max64(0, (int64_t)(segs - (double)nseq));   // not their sequence's last
+            const double t = unit * (spread(segs * h, mean + 0.7, c + 0.7) + 0.5 * spread(early * h, c + 1.4, c + 1.4)) +
+                             1.0 + 0.001 * early * (double)nheads / 2;
+            if (t < least) {
+                least = t;
+                best = {c, each};
+            }
         }
     }
-    return pick;
+    return best;
 }
 
 int64_t ssd_packed_places(int64_t tokens, int64_t nseq, int seg_chunks)
@@ -1172,7 +1184,7 @@ cudaError_t launch_ssd_packed(const SsdPackedParams &p, cudaStream_t stream)
                                  (int)kStSmemBytes);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(ssd_packed_places(p.tokens, p.nseq, p.seg_chunks) *
-                                          pairs_of(p.nheads, p.ngroups)));
+                                          pairs_of(p.nheads, p.ngroups, p.each)));
     ssd_packed_clear_kernel<<<1, 1, 0, stream>>>(p.status);
     e = cudaGetLastError();
     if (e == cudaSuccess && p.seg_chunks) {
