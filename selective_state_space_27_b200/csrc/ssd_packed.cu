@@ -47,8 +47,8 @@
 // them resumed, 182 us (38% of the time its bytes take; the longest prompts first,
 // so the SMs end within 3% of each other); 4 x 8192 tokens x 64 heads 237 us (the
 // dense kernel, one head per CTA: 385 us); one prompt of 32768 tokens x 24 heads
-// 143 us in segments, 44 + 8 + 95 us; three prompts of 378 tokens x 24 heads
-// 18.5 us on the device. A chunk of a pair of heads takes about 6800 clocks, of
+// 137 us in segments, 40 + 8 + 95 us; three prompts of 378 tokens x 24 heads 14 us
+// (13 on the device; 18 with two heads per CTA). A chunk of a pair of heads takes about 6800 clocks, of
 // which the tensor core works 3072. What bounds it is the chain w X - state
 // product - next state - C H^T together with shared memory, which is about 75%
 // busy with the products' operands (2304 clocks), TMA (1024) and the arithmetic
@@ -124,9 +124,10 @@ enum Bar { kFull, kXFull0, kXFull1, kGFull, kWReady, kMReady, kSFull, kYFull, kY
 constexpr uint32_t kOffTmem = kNumBars * 8;             // behind the barriers: tensor memory address, abort flag
 constexpr uint32_t kSmemBytes = kOffBar + kOffTmem + 16;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-// The states kernel: X once, B and both terms of w X twice (the products of one
-// chunk run while the next one's w X is made).
-constexpr uint32_t kStB = 2 * kAtom, kStW = 6 * kAtom, kStL = 10 * kAtom, kStStep = 14 * kAtom;
+// The states kernel: X three times, where the hi term of w X takes its place, B and
+// the lo term twice (the products of one chunk run while the next one's w X is made
+// and the one after that is loaded).
+constexpr uint32_t kStB = 6 * kAtom, kStL = 10 * kAtom, kStStep = 14 * kAtom;
 struct alignas(16) StateStep {
     float w[kQ], decay;   // 2^(s to the segment's end) delta_i; decay from this chunk to the segment's end
 };
@@ -466,10 +467,11 @@ __device__ __forceinline__ void teardown(uint32_t tmem)
 // zero for the others, and its decay. Chunks run from the segment's end to its
 // start: the decay of what follows a chunk is then a sum that ends at the
 // segment's end, the weights count to there and the chunks' products add up
-// without rescaling. Its barriers: xfull0 X, mready X read, gfull / yfull B (by
-// buffer), wready, step (by buffer and head) and sfree (by buffer: the products of
-// the chunk are done) as above; each one's next phase needs what its waiters do
-// next.
+// without rescaling. Its barriers: xfull0 / xfull1 / sfull X (by
+// place), gfull / yfull B (by buffer), wready, step (by buffer and head) and sfree
+// (by buffer: the products of the chunk are done) as above; each one's next phase
+// needs what its waiters do next. (X loaded into one place when it had been read:
+// 44 us against 40 for 32768 tokens x 24 heads.)
 __global__ void __launch_bounds__(kThreads, 1)
 ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap b_map,
                          const SsdPackedParams p)
@@ -494,6 +496,9 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
                       p.wait_limit_ns};
     auto phase = [](int i) { return (uint32_t)(i >> 1) & 1u; };   // of the barriers with two buffers
     auto bfull = [](int i) { return i & 1 ? kYFull : kGFull; };
+    auto xfull = [](int i) { return i % 3 == 0 ? kXFull0 : i % 3 == 1 ? kXFull1 : kSFull; };
+    auto xphase = [](int i) { return (uint32_t)(i / 3) & 1u; };
+    auto xplace = [&](int i) { return base + (uint32_t)(2 * (i % 3)) * kAtom; };
 
     if (warp == kStepWarp || warp == kStepWarp + 1) {
         const int head = warp - kStepWarp, h = hp.h + head;
@@ -540,6 +545,16 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
         }
     } else if (warp == kTmaWarp) {
         int bs = 0, xs = 0;   // chunks whose B, and whose X, are on their way
+        auto load_x = [&](int i) {
+            if (lane == 0) {
+                mbar_arrive_tx(bar(xfull(i)), (uint32_t)hp.nh * kAtom);
+                for (int j = 0; j < hp.nh; ++j)
+                    tma_load_2d(xplace(i) + (uint32_t)j * kAtom, &x_map, bar(xfull(i)), (hp.h + j) * kP,
+                                g.row + (K - 1 - i) * kQ);
+            }
+            xs = i + 1;
+        };
+        if (K > 0) load_x(0);
         for (int i = 0; i < K; ++i) {
             const int row = g.row + (K - 1 - i) * kQ;
             if (i >= 2 && !wait.go(kSFree0 + (i & 1), phase(i - 2))) break;
@@ -550,19 +565,11 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
                 tma_load_2d(b + kAtom, &b_map, full, hp.group * kN + 64, row);
             }
             bs = i + 1;
-            if (i > 0 && !wait.go(kMReady, (i - 1) & 1)) break;
-            if (lane == 0) {
-                mbar_arrive_tx(bar(kXFull0), (uint32_t)hp.nh * kAtom);
-                for (int j = 0; j < hp.nh; ++j) {
-                    tma_load_2d(base + (uint32_t)j * kAtom, &x_map, bar(kXFull0), (hp.h + j) * kP, row);
-                    if (i + 1 < K) tma_prefetch_2d(&x_map, (hp.h + j) * kP, row - kQ);
-                }
-            }
-            xs = i + 1;
+            if (i + 1 < K) load_x(i + 1);   // (its place was free with chunk i - 2's products, too)
             __syncwarp();
         }
         if (lane == 0) {   // loads in flight must land
-            if (xs) mbar_wait(bar(kXFull0), (xs - 1) & 1);
+            for (int i = max(0, xs - 3); i < xs; ++i) mbar_wait(bar(xfull(i)), xphase(i));
             for (int i = max(0, bs - 2); i < bs; ++i) mbar_wait(bar(bfull(i)), phase(i));
         }
         __syncwarp();
@@ -573,7 +580,7 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
                 wait.one(kWReady, i & 1);
                 tc_after_sync();
                 const uint32_t two = (uint32_t)(2 * (i & 1)) * kAtom;
-                issue_state_product(tmem, base + kStB + two, base + kStW + two, base + kStL + two, i > 0);
+                issue_state_product(tmem, base + kStB + two, xplace(i), base + kStL + two, i > 0);
                 mma_commit(bar(kSFree0 + (i & 1)));
             }
             mma_commit(bar(kDrain));   // every MMA must finish before the tensor memory is freed
@@ -587,23 +594,18 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
         const float *cache = resumed ? p.state + slot * p.s_slot + (int64_t)h * (kP * kN) : nullptr;
         for (int i = 0; i < K; ++i) {
             wait(kStep0 + 2 * (i & 1) + head, phase(i));
-            wait(kXFull0, i & 1);
+            wait(xfull(i), xphase(i));
             const float w = step[2 * (i & 1) + head].w[r];
-            const uint32_t tiles = (uint32_t)(2 * (i & 1) + head) * kAtom;
-            uint4 x[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                x[q] = ld_shared_v4(base + (uint32_t)head * kAtom + sw128((uint32_t)r, (uint32_t)(4 * hq + q)));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kMReady));   // X was read: the next chunk's may come
+            const uint32_t xt = xplace(i) + (uint32_t)head * kAtom;
+            const uint32_t lt = base + kStL + (uint32_t)(2 * (i & 1) + head) * kAtom;
             if (i >= 2) wait(kSFree0 + (i & 1), phase(i - 2));
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint32_t at = tiles + sw128((uint32_t)r, (uint32_t)(4 * hq + q));
+                const uint32_t at = sw128((uint32_t)r, (uint32_t)(4 * hq + q));
                 uint32_t hi[4], lo[4];
-                split(x[q], w, hi, lo);
-                st_shared_v4(base + kStW + at, hi[0], hi[1], hi[2], hi[3]);
-                st_shared_v4(base + kStL + at, lo[0], lo[1], lo[2], lo[3]);
+                split(ld_shared_v4(xt + at), w, hi, lo);
+                st_shared_v4(xt + at, hi[0], hi[1], hi[2], hi[3]);
+                st_shared_v4(lt + at, lo[0], lo[1], lo[2], lo[3]);
             }
             async_proxy_fence();
             __syncwarp();

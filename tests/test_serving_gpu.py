@@ -302,17 +302,23 @@ def test_ssd_packed_reports_a_wait_that_ran_out(ms, lens, H, must):
     """A limit of a microsecond: the call ends, says whether a wait ran out, and leaves nothing behind.
     The step warps run four chunks ahead and then wait for each chunk's products: 48 MMAs of 64 clocks for two
     heads, 1.6 us at 1965 MHz, less a step's own quarter of a microsecond. Where 256 pairs of heads share 148 SMs
-    a CTA takes two heads and some wait must run out; where the CTAs have room, a chunk of one head may take
-    less than the limit and the call may end well."""
+    a CTA takes two heads and waits run out, though the device's timer may step too rarely to show it in every
+    call; where the CTAs have room, a chunk of one head may take less than the limit."""
     g = rng(47)
     _, cu = offsets(lens)
     a, kw, _ = ssd_inputs(g, sum(lens), H, 1, False)
     want = ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=max(lens), **kw)
-    try:
-        got = ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=max(lens), wait_limit_us=1, **kw)
-        assert not must and torch.equal(got, want)
-    except ms.MambaScanError as e:
-        assert e.status == 5                                 # MS_ERR_TIMEOUT
+    ran_out = 0
+    for _ in range(300 if must else 3):
+        try:
+            got = ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=max(lens), wait_limit_us=1, **kw)
+            assert torch.equal(got, want)
+        except ms.MambaScanError as e:
+            assert e.status == 5                             # MS_ERR_TIMEOUT
+            ran_out += 1
+        if ran_out and must:
+            break
+    assert ran_out or not must
     assert torch.equal(ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=max(lens), **kw), want)
 
 
