@@ -47,8 +47,8 @@
 // them resumed, 182 us (38% of the time its bytes take; the longest prompts first,
 // so the SMs end within 3% of each other); 4 x 8192 tokens x 64 heads 237 us (the
 // dense kernel, one head per CTA: 385 us); one prompt of 32768 tokens x 24 heads
-// 137 us in segments, 40 + 8 + 95 us; three prompts of 378 tokens x 24 heads 14 us
-// (13 on the device; 18 with two heads per CTA). A chunk of a pair of heads takes about 6800 clocks, of
+// 135 us in segments, 40 + 8 + 95 us one by one; three prompts of 378 tokens x 24
+// heads 11 us on the device, 14 with two heads per CTA. A chunk of a pair of heads takes about 6800 clocks, of
 // which the tensor core works 3072. What bounds it is the chain w X - state
 // product - next state - C H^T together with shared memory, which is about 75%
 // busy with the products' operands (2304 clocks), TMA (1024) and the arithmetic
@@ -359,9 +359,9 @@ __device__ __forceinline__ void split(const uint4 &xr, float w, uint32_t (&hi)[4
 
 // The state product B^T (w X) of both heads, hi then lo, onto what the accumulator holds or in its place.
 __device__ __forceinline__ void issue_state_product(uint32_t tmem, uint32_t b_tile, uint32_t hi_tile, uint32_t lo_tile,
-                                                    bool onto)
+                                                    bool onto, int nh)
 {
-    constexpr uint32_t id_s = bf16_idesc(128, 128, true, true);
+    const uint32_t id_s = bf16_idesc(128, 64 * nh, true, true);
     const uint64_t b = sw128_desc(b_tile, kAtom, 1024);
     const uint64_t hi = sw128_desc(hi_tile, kAtom, 1024), lo = sw128_desc(lo_tile, kAtom, 1024);
 #pragma unroll
@@ -468,10 +468,12 @@ __device__ __forceinline__ void teardown(uint32_t tmem)
 // start: the decay of what follows a chunk is then a sum that ends at the
 // segment's end, the weights count to there and the chunks' products add up
 // without rescaling. Its barriers: xfull0 / xfull1 / sfull X (by
-// place), gfull / yfull B (by buffer), wready, step (by buffer and head) and sfree
-// (by buffer: the products of the chunk are done) as above; each one's next phase
-// needs what its waiters do next. (X loaded into one place when it had been read:
-// 44 us against 40 for 32768 tokens x 24 heads.)
+// place), gfull / yfull B, wready / hready w X, step and sfree (the products of the
+// chunk are done), these by buffer. No waiter falls two phases behind: the next
+// phase of each needs the products of its buffer's last chunk, which need every
+// wait for that chunk (w X of chunk i + 1 may be ready before B of chunk i has
+// come, so one barrier for both buffers would not do). X loaded into one place once
+// it had been read took 44 us against 40 for 32768 tokens x 24 heads.
 __global__ void __launch_bounds__(kThreads, 1)
 ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap b_map,
                          const SsdPackedParams p)
@@ -496,6 +498,7 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
                       p.wait_limit_ns};
     auto phase = [](int i) { return (uint32_t)(i >> 1) & 1u; };   // of the barriers with two buffers
     auto bfull = [](int i) { return i & 1 ? kYFull : kGFull; };
+    auto wready = [](int i) { return i & 1 ? kHReady : kWReady; };
     auto xfull = [](int i) { return i % 3 == 0 ? kXFull0 : i % 3 == 1 ? kXFull1 : kSFull; };
     auto xphase = [](int i) { return (uint32_t)(i / 3) & 1u; };
     auto xplace = [&](int i) { return base + (uint32_t)(2 * (i % 3)) * kAtom; };
@@ -577,10 +580,10 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
         if (lane == 0) {
             for (int i = 0; i < K; ++i) {
                 wait.one(bfull(i), phase(i));
-                wait.one(kWReady, i & 1);
+                wait.one(wready(i), phase(i));
                 tc_after_sync();
                 const uint32_t two = (uint32_t)(2 * (i & 1)) * kAtom;
-                issue_state_product(tmem, base + kStB + two, xplace(i), base + kStL + two, i > 0);
+                issue_state_product(tmem, base + kStB + two, xplace(i), base + kStL + two, i > 0, hp.nh);
                 mma_commit(bar(kSFree0 + (i & 1)));
             }
             mma_commit(bar(kDrain));   // every MMA must finish before the tensor memory is freed
@@ -609,7 +612,7 @@ ssd_packed_states_kernel(const __grid_constant__ CUtensorMap x_map, const __grid
             }
             async_proxy_fence();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kWReady));
+            if (lane == 0) mbar_arrive(bar(wready(i)));
         }
         wait(kSFree0 + ((K - 1) & 1), phase(K - 1));
         dependents_may_start();
@@ -862,7 +865,7 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
         // ---- MMA issue (one thread) ----
         if (lane == 0) {
             constexpr uint32_t id_g = bf16_idesc(128, 128, false, false);   // G = C B^T
-            constexpr uint32_t id_o = bf16_idesc(128, 128, false, true);    // C H^T, both heads
+            const uint32_t id_o = bf16_idesc(128, 64 * hp.nh, false, true); // C H^T of the heads
             constexpr uint32_t id_y = bf16_idesc(128, 64, false, true);     // M' X
             const uint64_t dc = sw128_desc(base + kOffC, 16, 1024), db = sw128_desc(base + kOffB, 16, 1024);
             const uint64_t dh = sw128_desc(base + kOffH, kAtom, 1024), dx = sw128_desc(base + kOffX, kAtom, 1024);
@@ -887,7 +890,7 @@ ssd_packed_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_consta
                 mma_commit(bar(kGFull));
                 wait.one(kWReady, k & 1);
                 tc_after_sync();
-                issue_state_product(tmem, base + kOffB, base + kOffW, base + kOffH, true);
+                issue_state_product(tmem, base + kOffB, base + kOffW, base + kOffH, true, hp.nh);
                 mma_commit(bar(kSFull));
                 wait.one(kMReady, k & 1);
                 tc_after_sync();

@@ -322,6 +322,34 @@ def test_ssd_packed_reports_a_wait_that_ran_out(ms, lens, H, must):
     assert torch.equal(ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=max(lens), **kw), want)
 
 
+@pytest.mark.parametrize("lens,H", [([32768], 24), ([5000, 1, 0, 20000], 3), ([200, 150, 28], 24)])
+def test_ssd_packed_many_calls_in_a_graph(ms, lens, H):
+    """Calls one right behind the other, with one workspace: no wait runs out, every call gives the same."""
+    g = rng(59)
+    _, cu = offsets(lens)
+    a, kw, _ = ssd_inputs(g, sum(lens), H, 1, False)
+    state = torch.zeros(len(lens), H, 64, 128, device="cuda")
+    out = torch.zeros(sum(lens), H, 64, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+
+    def call():
+        ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=max(lens), state=state, out=out, workspace=ws, check=False, **kw)
+
+    call()
+    ms.ssd_check(ws)
+    want = out.clone(), state.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(20):
+            call()
+    for _ in range(20):
+        out.fill_(float("nan"))
+        state.fill_(float("nan"))
+        graph.replay()
+        ms.ssd_check(ws)
+        assert torch.equal(out, want[0]) and torch.equal(state, want[1])
+
+
 def test_cache_beyond_32_bits(ms):
     """Slots whose offset in the cache passes 2^31 elements (8 GB of states)."""
     g = rng(53)
