@@ -21,7 +21,9 @@
 // core. One CTA per SM therefore walks one segment (see below) of TWO heads of
 // one group: they share B, C and G, and C H^T and B^T (w X) are products with
 // N = 128. Per chunk and pair of heads 48 MMAs, 3072 clocks, against 5120 one by
-// one. 512 columns of tensor memory: G; M' of both heads (the A operand of
+// one. Where the SMs have room for a CTA per head, each takes ONE head: its chunk
+// still takes 0.7 of the time, with half the arithmetic and shared-memory traffic
+// (measured; ssd_packed_plan). 512 columns of tensor memory: G; M' of both heads (the A operand of
 // M' X); Y and the states of both. 208 KB of shared memory: X twice (the next
 // chunk's loads while this one is worked on), B, C, the split w X and the
 // states' bf16 copies, whose place the lo term of w X takes between C H^T and
@@ -36,7 +38,7 @@
 // their buffer was read for the last time.
 //
 // Long sequences with few heads are cut into segments that run side by side
-// (ssd_packed_segment): a first kernel computes what every segment but a
+// (ssd_packed_plan): a first kernel computes what every segment but a
 // sequence's last adds to the state from zero (the state product alone), a
 // second one adds these up along each sequence, a third one does the rest from
 // the state that its segment starts from. The kernels of a call follow each other
@@ -1100,7 +1102,10 @@ bool encode_rows(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, i
 
 }  // namespace
 
-// A chunk of one head takes kOneHead of the time of a chunk of two.
+// A chunk of one head takes kOneHead of the time of a chunk of two (4096 tokens x
+// 128 heads, a CTA per head against one per pair: 98 against 142 us; 512 tokens x
+// 24 heads 16 against 20 us; where a CTA per head fills the SMs more than once the
+// pairs win: 8192 tokens x 64 heads 105 against 186 us in segments).
 constexpr double kOneHead = 0.7;
 
 // Chunks per segment (0: sequences are not cut) and heads per CTA: the smallest
