@@ -43,7 +43,8 @@ def up_to_date() -> bool:
 
 
 def binding_up_to_date() -> bool:
-    return _newer(BINDING, [os.path.join(CSRC, "binding.cpp"), os.path.abspath(__file__)])
+    return _newer(BINDING, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "mambascan.h"),
+                            os.path.abspath(__file__)])
 
 
 def _newer(target, files) -> bool:
@@ -59,7 +60,7 @@ def build_binding(verbose: bool = False) -> str:
                sysconfig.get_paths()["include"]]
     tmp = BINDING + f".{os.getpid()}.tmp"
     cmd = [os.environ.get("CXX") or "g++", "-shared", "-fPIC", "-O2", "-std=c++17",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in include),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in [INCLUDE, *include]),
            os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python",
            "-ltorch_cpu", "-lc10"]
     if verbose:

@@ -3,9 +3,9 @@
 The calls that a serving step makes for every layer: on small batches they are
 bound by the host, so this module marshals lean. Tensors are checked once, by the
 compiled ``_binding`` (``csrc/binding.cpp``), and their pointers and strides packed
-into the C structs of ``include/mambascan.h`` with :mod:`struct`; the structs'
-ctypes mirrors (``ConvPackedArgs`` and so on) describe the same layouts. Outputs
-are allocated here unless ``out`` is given.
+into the C structs of ``include/mambascan.h`` with :mod:`struct` (the norms' in the
+compiled module); the structs' ctypes mirrors (``ConvPackedArgs`` and so on) describe
+the same layouts. Outputs are allocated by the call unless ``out`` is given.
 """
 from __future__ import annotations
 
@@ -17,6 +17,7 @@ import torch
 from . import (MS_BF16, MS_F32, SSD_DSTATE, SSD_HEADDIM, MambaScanError, load_library, ssd_check)
 
 try:
+    from . import _binding
     from ._binding import empty_like as _empty_like, rows as _rows, scratch as _scratch, vector as _vector
 except ImportError as e:
     raise RuntimeError("the compiled tensor checks are not built or do not fit this torch "
@@ -27,8 +28,6 @@ CONV_PACKED = struct.Struct("@4q2i Pq Pq Pqq PPP")
 CONV1D = struct.Struct("@PPii")
 SSD_PACKED = struct.Struct("@6q2i Pq Pq Pq Pq Pq Pq PPP Pq PPP Ii")
 SSD_UPDATE = struct.Struct("@6q2i Pq Pq Pq Pq Pq Pq Pq PPPP")
-NORM = struct.Struct("@3q2i2f2i Pq Pq Pq Pq Pq P")
-NORM_BWD = struct.Struct("@Pq Pq Pq Pq Pq P")
 
 _F32 = torch.float32
 _DTYPES = {torch.float32: MS_F32, torch.bfloat16: MS_BF16}
@@ -46,6 +45,28 @@ def _fn(name, *argtypes):
         f.argtypes = argtypes
         _fns[name] = f
     return f
+
+
+_addresses = {}
+
+
+def _address(name):
+    """Address of an entry point, for the calls that the compiled module makes itself."""
+    a = _addresses.get(name)
+    if a is None:
+        a = _addresses[name] = ctypes.cast(load_library()[name], ctypes.c_void_p).value
+    return a
+
+
+def _stream(x, stream):
+    """Handle of ``stream`` or of the current stream of x's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if not x.is_cuda:
+        return 0
+    if _raw_stream is not None:
+        return _raw_stream(x.device.index)
+    return torch.cuda.current_stream(x.device).cuda_stream
 
 
 _str, _ptr, _size = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t
@@ -277,12 +298,6 @@ def ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_sof
 
 # ---- norm ----------------------------------------------------------------------
 
-def _residual_code(t, dtype):
-    if t.dtype is not dtype and t.dtype is not torch.float32:
-        raise TypeError(f"the residual must be {dtype} or torch.float32, got {t.dtype}")
-    return _DTYPES[t.dtype]
-
-
 def norm_fwd(x, weight=None, z=None, residual=None, residual_scale=1.0, eps=1e-5, group_size=None, gate_first=True,
              out=None, residual_out=None, stream=None):
     """RMS norm of each row's groups of ``group_size`` channels (None: the row).
@@ -294,25 +309,14 @@ def norm_fwd(x, weight=None, z=None, residual=None, residual_scale=1.0, eps=1e-5
     rows of any stride; weight (dim,) float32 or None. Returns ``(y,
     residual_out)``, residual_out None without a residual.
     """
-    device, code = _cuda(x, 2, "x")
-    dtype = x.dtype
-    rows, dim = shape = x.shape
-    y = _empty_like(x) if out is None else out
-    res_code, res, ro = code, (0, 0), (0, 0)
-    if residual is not None:
-        res_code = _residual_code(residual, dtype)
-        if residual_out is None:
-            residual_out = _empty_like(residual)
-        res = _rows("residual", residual, residual.dtype, shape, device)
-        ro = _rows("residual_out", residual_out, residual.dtype, shape, device)
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    args = NORM.pack(rows, dim, dim if group_size is None else group_size, code, res_code, eps, residual_scale,
-                     1 if gate_first else 0, 0, *_rows("x", x, dtype, shape, device),
-                     *_rows("z", z, dtype, shape, device), *res, *ro, *_rows("out", y, dtype, shape, device),
-                     _vector("weight", weight, dim, device, _F32))
-    _run(device, stream, _fn("mamba_norm_fwd", _str, _ptr), args)
-    return y, residual_out
+    if x.is_cuda and x.device.index != _current_device():
+        with torch.cuda.device(x.device):
+            return norm_fwd(x, weight, z, residual, residual_scale, eps, group_size, gate_first, out, residual_out, stream)
+    status, y, total = _binding.norm_fwd(_address("mamba_norm_fwd"), _stream(x, stream), x, weight, z, residual,
+                                         residual_scale, eps, group_size, gate_first, out, residual_out)
+    if status:
+        raise MambaScanError(status, load_library().mamba_last_error().decode(errors="replace"))
+    return y, total
 
 
 def norm_bwd(dy, x, weight=None, z=None, residual_out=None, dresidual_out=None, residual_scale=1.0, eps=1e-5,
@@ -325,37 +329,15 @@ def norm_bwd(dy, x, weight=None, z=None, residual_out=None, dresidual_out=None, 
     in the residual's, dweight (dim,) float32 (None without weight).
     ``workspace``: optional uint8 CUDA tensor, allocated here when needed.
     """
-    device, code = _cuda(x, 2, "x")
-    dtype = x.dtype
-    rows, dim = shape = x.shape
-    out = {"dx": _empty_like(x), "dz": None, "dresidual": None, "dweight": None}
-    res_code, ro, dro, dres, dz = code, (0, 0), (0, 0), (0, 0), (0, 0)
-    if residual_out is not None:
-        res_code = _residual_code(residual_out, dtype)
-        ro = _rows("residual_out", residual_out, residual_out.dtype, shape, device)
-        dro = _rows("dresidual_out", dresidual_out, residual_out.dtype, shape, device)
-        out["dresidual"] = _empty_like(residual_out)
-        dres = out["dresidual"].data_ptr(), dim
-    elif dresidual_out is not None:
-        raise ValueError("dresidual_out needs residual_out")
-    if z is not None:
-        out["dz"] = _empty_like(x)
-        dz = out["dz"].data_ptr(), dim
-    dw = 0
-    if weight is not None:
-        out["dweight"] = torch.empty(dim, dtype=torch.float32, device=device)
-        dw = out["dweight"].data_ptr()
-    args = NORM.pack(rows, dim, dim if group_size is None else group_size, code, res_code, eps, residual_scale,
-                     1 if gate_first else 0, 0, *_rows("x", x, dtype, shape, device),
-                     *_rows("z", z, dtype, shape, device), 0, 0, *ro, 0, 0, _vector("weight", weight, dim, device, _F32))
-    grads = NORM_BWD.pack(*_rows("dy", dy, dtype, shape, device), *dro, out["dx"].data_ptr(), dim, *dz, *dres, dw)
-    ws, own = None, False
-    if dw:
-        need = _workspace_bytes(device, "mamba_norm_bwd_workspace_size", args)
-        if need:
-            ws, own = _workspace(x, workspace, need)
-    _run(device, stream, _fn("mamba_norm_bwd", _str, _str, _ptr, _size, _ptr), args, grads,
-         0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
-    if own:
-        _keep(ws, stream)
-    return out
+    if x.is_cuda and x.device.index != _current_device():
+        with torch.cuda.device(x.device):
+            return norm_bwd(dy, x, weight, z, residual_out, dresidual_out, residual_scale, eps, group_size, gate_first,
+                            workspace, stream)
+    status, dx, dz, dresidual, dweight, scratch = _binding.norm_bwd(
+        _address("mamba_norm_bwd"), _address("mamba_norm_bwd_workspace_size"), _stream(x, stream), dy, x, weight, z,
+        residual_out, dresidual_out, residual_scale, eps, group_size, gate_first, workspace)
+    if status:
+        raise MambaScanError(status, load_library().mamba_last_error().decode(errors="replace"))
+    if scratch is not None:
+        _keep(scratch, stream)
+    return {"dx": dx, "dz": dz, "dresidual": dresidual, "dweight": dweight}

@@ -731,6 +731,20 @@ def test_python_refusals(ms):
         ms.norm_fwd(f(4, 8), residual=f(4, 8, dtype=bf))
     with pytest.raises(ValueError):
         ms.norm_fwd(f(4, 8), residual_out=f(4, 8))
+    for kind, bad in ((TypeError, dict(z=f(4, 8, dtype=bf))), (ValueError, dict(z=f(4, 9))), (ValueError, dict(weight=f(9))),
+                      (TypeError, dict(weight=f(8, dtype=bf))), (ValueError, dict(out=torch.zeros(4, 8))),
+                      (ValueError, dict(z=f(8, 4).t())), (TypeError, dict(eps="x")), (TypeError, dict(z=3)), (TypeError, dict(group_size=2.5)),
+                      (ValueError, dict(weight=f(16)[::2]))):
+        with pytest.raises(kind):
+            ms.norm_fwd(f(4, 8), **bad)
+    with pytest.raises(ValueError):
+        ms.norm_fwd(f(8))
+    with pytest.raises(TypeError):
+        ms.norm_fwd(f(4, 8, dtype=torch.float16))
+    with pytest.raises(ValueError):
+        ms.norm_bwd(f(4, 8), f(4, 8), weight=f(8), workspace=f(100))
+    with pytest.raises(ValueError):
+        ms.norm_bwd(f(4, 9), f(4, 8))
     with pytest.raises(ms.MambaScanError):
         ms.norm_fwd(f(4, 8), group_size=3)
     with pytest.raises(ValueError):
