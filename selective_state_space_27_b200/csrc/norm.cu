@@ -667,7 +667,7 @@ cudaError_t bwd_vec(const NormParams &p0, const NormBwdParams &g, cudaStream_t s
                 constexpr int row = stages_of<T, R, VEC, NV, MODE>() * NV * BwdVec<T, R, VEC, MODE>::kBytes;
                 const auto launch = [&](auto kernel, int threads, int64_t share) {
                     const size_t smem = static_cast<size_t>(row) * threads + static_cast<size_t>(share + 3) / 4 * 16;
-                    if (smem > 48 * 1024) {
+                    if (smem > 47 * 1024) {   // (the kernel's own 256 bytes count, too)
                         const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                                    static_cast<int>(smem));
                         if (a != cudaSuccess) return a;

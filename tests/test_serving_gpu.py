@@ -474,6 +474,13 @@ def test_norm_bwd(ms, rows, dim, group, dtype, residual, gate, first, weight, la
     (9001, 512, 512, "bf16", None, True, True), (2500, 1530, 1530, "f32", "f32", False, True),
     (750, 16384, 16384, "bf16", None, True, False), (1999, 2048, 2048, "bf16", "f32", False, True),
     (20011, 48, 16, "bf16", "bf16", False, True), (1200, 4096, 4096, "f32", None, False, True),
+    # every number of vectors per thread, for warps and blocks, with the most bytes per row on their way
+    (64, 2048, 2048, "f32", "f32", False, True), (300, 1024, 512, "f32", "f32", False, True),
+    (300, 512, 256, "f32", "f32", False, True), (70, 8192, 8192, "f32", "f32", False, True),
+    (70, 16384, 16384, "f32", None, True, True), (90, 4096, 4096, "bf16", "f32", False, True),
+    (90, 8192, 8192, "bf16", "f32", False, True), (90, 8192, 8192, "bf16", None, True, True),
+    (90, 2048, 1024, "bf16", "bf16", False, True), (200, 640, 128, "bf16", "f32", False, True),
+    (200, 66, 66, "f32", "f32", False, True), (100, 3330, 3330, "f32", None, True, False),
 ])
 def test_norm_bwd_many_rows(ms, rows, dim, group, dtype, residual, gate, first):
     """More rows than a team of threads has on their way together."""
