@@ -684,7 +684,8 @@ typedef struct ms_ssd_packed_args {
 ms_status mamba_ssd_packed_workspace_size(const ms_ssd_packed_args *args, size_t *bytes);
 
 /*
- * One kernel launch on `stream`, or three when sequences are cut. The workspace
+ * Two kernel launches on `stream` (the first clears the status word), or four when
+ * sequences are cut. The workspace
  * (256-byte aligned, of at least mamba_ssd_packed_workspace_size bytes) starts
  * with a status word with mamba_ssd_fwd's meaning: 0 after a normal run,
  * MS_ERR_TIMEOUT when an internal wait gave up (outputs and states then hold

@@ -20,7 +20,7 @@
 // (measured), so a product with N = 64, one head, wastes half of the tensor
 // core. One CTA per SM therefore walks one segment (see below) of TWO heads of
 // one group: they share B, C and G, and C H^T and B^T (w X) are products with
-// N = 128. Per chunk and pair of heads 48 MMAs, 3072 clocks, against 5120 one by
+// N = 128. Per chunk and pair of heads 48 MMAs of 64 clocks, against 80 one by
 // one. Where the SMs have room for a CTA per head, each takes ONE head: its chunk
 // still takes 0.7 of the time, with half the arithmetic and shared-memory traffic
 // (measured; ssd_packed_plan). 512 columns of tensor memory: G; M' of both heads (the A operand of
@@ -51,7 +51,7 @@
 // dense kernel, one head per CTA: 385 us); one prompt of 32768 tokens x 24 heads
 // 135 us in segments, 40 + 8 + 95 us one by one; three prompts of 378 tokens x 24
 // heads 11 us on the device, 14 with two heads per CTA. A chunk of a pair of heads takes about 6800 clocks, of
-// which the tensor core works 3072. What bounds it is the chain w X - state
+// which the tensor core works 45%. What bounds it is the chain w X - state
 // product - next state - C H^T together with shared memory, which is about 75%
 // busy with the products' operands (2304 clocks), TMA (1024) and the arithmetic
 // warps' own accesses (1800), so that arithmetic beside the products slows both.
