@@ -4,14 +4,16 @@
 // the calls with the least work per tensor, are marshalled here altogether.
 //   rows(name, t, dtype, shape, device) -> (pointer, stride of the first axis)
 //   vector(name, t, n, device, dtype)   -> pointer
-//   empty_like(t), scratch(bytes, t)    -> uninitialised tensors on t's device
+//   empty_like(t)                       -> an uninitialised tensor like it
 //   norm_fwd(entry point, stream, arguments of serving.norm_fwd) -> (status, y, residual_out)
 //   norm_bwd(entry point, its workspace query, stream, arguments) -> (status, dx, dz, dresidual, dweight, scratch)
+//   ssd_packed(entry point, its workspace query, stream, packed arguments, x, workspace) -> (status, workspace used)
 // A None tensor has pointer and stride 0; what does not fit raises ValueError or,
 // for a type, TypeError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <cstring>
 #include <string>
 
 #include <ATen/ATen.h>
@@ -143,15 +145,6 @@ PyObject *empty_like(PyObject *, PyObject *t) {
     if (!is_tensor(Py_None, t)) return nullptr;
     const at::Tensor &x = THPVariable_Unpack(t);
     return THPVariable_Wrap(at::empty(x.sizes(), x.options()));
-    END_HANDLE_TH_ERRORS
-}
-
-PyObject *scratch(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    HANDLE_TH_ERRORS
-    if (!arguments(n, 2) || !is_tensor(Py_None, a[1])) return nullptr;
-    const long long bytes = PyLong_AsLongLong(a[0]);
-    if (bytes == -1 && PyErr_Occurred()) return nullptr;
-    return THPVariable_Wrap(at::empty({bytes}, THPVariable_Unpack(a[1]).options().dtype(at::kByte)));
     END_HANDLE_TH_ERRORS
 }
 
@@ -342,19 +335,60 @@ PyObject *norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// The workspace's size, a workspace of that size where none large enough is given, and the call.
+PyObject *ssd_packed(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 6)) return nullptr;
+    try {
+        const auto fn = entry<ms_status (*)(const ms_ssd_packed_args *, void *, size_t, void *)>(a[0]);
+        const auto query = entry<ms_status (*)(const ms_ssd_packed_args *, size_t *)>(a[1]);
+        void *stream = PyLong_AsVoidPtr(a[2]);
+        char *bytes = nullptr;
+        Py_ssize_t length = 0;
+        if (PyBytes_AsStringAndSize(a[3], &bytes, &length) < 0 || PyErr_Occurred()) return nullptr;
+        const at::Tensor *x = optional("x", a[4]), *given = optional("workspace", a[5]);
+        if (!x || length != sizeof(ms_ssd_packed_args)) throw Refused{PyExc_ValueError, "the packed arguments do not fit"};
+        ms_ssd_packed_args p;
+        std::memcpy(&p, bytes, sizeof(p));
+        if (given && (given->scalar_type() != at::kByte || given->device() != x->device() || !given->is_contiguous()))
+            throw Refused{PyExc_ValueError, "workspace must be a contiguous uint8 tensor on " + x->device().str()};
+        size_t need = 0;
+        ms_status status = query(&p, &need);
+        at::Tensor space;
+        if (status == MS_OK) {
+            space = given && static_cast<size_t>(given->numel()) >= need
+                        ? *given
+                        : at::empty({static_cast<int64_t>(need)}, x->options().dtype(at::kByte));
+            void *at = space.data_ptr();
+            const size_t size = static_cast<size_t>(space.numel());
+            Py_BEGIN_ALLOW_THREADS
+            status = fn(&p, at, size, stream);
+            Py_END_ALLOW_THREADS
+        }
+        PyObject *r = PyTuple_New(2);
+        if (!r) return nullptr;
+        PyTuple_SET_ITEM(r, 0, PyLong_FromLong(status));
+        PyTuple_SET_ITEM(r, 1, space.defined() ? THPVariable_Wrap(space) : Py_NewRef(Py_None));
+        return r;
+    } catch (const Refused &r) {
+        return raise(r);
+    }
+    END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(rows)), METH_FASTCALL,
      "rows(name, t, dtype, shape, device): (pointer, stride of the first axis)."},
     {"vector", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(vector)), METH_FASTCALL,
      "vector(name, t, n, device, dtype): pointer."},
     {"empty_like", empty_like, METH_O, "An uninitialised contiguous tensor of t's sizes, type and device."},
-    {"scratch", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(scratch)), METH_FASTCALL,
-     "scratch(bytes, t): uninitialised bytes on t's device."},
     {"norm_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(norm_fwd)), METH_FASTCALL,
      "norm_fwd(entry point, stream, x, weight, z, residual, scale, eps, group_size, gate_first, out, residual_out)."},
     {"norm_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(norm_bwd)), METH_FASTCALL,
      "norm_bwd(entry point, query, stream, dy, x, weight, z, residual_out, dresidual_out, scale, eps, group_size, "
      "gate_first, workspace)."},
+    {"ssd_packed", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(ssd_packed)), METH_FASTCALL,
+     "ssd_packed(entry point, query, stream, packed arguments, x, workspace)."},
     {nullptr, nullptr, 0, nullptr},
 };
 

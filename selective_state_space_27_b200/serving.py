@@ -18,7 +18,7 @@ from . import (MS_BF16, MS_F32, SSD_DSTATE, SSD_HEADDIM, MambaScanError, load_li
 
 try:
     from . import _binding
-    from ._binding import empty_like as _empty_like, rows as _rows, scratch as _scratch, vector as _vector
+    from ._binding import empty_like as _empty_like, rows as _rows, vector as _vector
 except ImportError as e:
     raise RuntimeError("the compiled tensor checks are not built or do not fit this torch "
                        "(run python -m selective_state_space_27_b200.build)") from e
@@ -69,7 +69,7 @@ def _stream(x, stream):
     return torch.cuda.current_stream(x.device).cuda_stream
 
 
-_str, _ptr, _size = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t
+_str, _ptr = ctypes.c_char_p, ctypes.c_void_p
 
 
 def _run(device, stream, fn, *args):
@@ -86,29 +86,6 @@ def _run(device, stream, fn, *args):
     status = fn(*args, s)
     if status:
         raise MambaScanError(status, load_library().mamba_last_error().decode(errors="replace"))
-
-
-def _workspace_bytes(device, name, args):
-    """Bytes that a workspace query reports for the packed ``args`` on ``device``."""
-    if device.index != _current_device():
-        with torch.cuda.device(device):
-            return _workspace_bytes(device, name, args)
-    n = _size(0)
-    status = _fn(name, _str, ctypes.POINTER(_size))(args, ctypes.byref(n))
-    if status:
-        raise MambaScanError(status, load_library().mamba_last_error().decode(errors="replace"))
-    return n.value
-
-
-def _workspace(x, workspace, need):
-    """(tensor on x's device, whether it was allocated here) of at least ``need`` bytes."""
-    if workspace is not None:
-        device = x.device
-        if workspace.dtype is not torch.uint8 or workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
-        if workspace.numel() >= need:
-            return workspace, False
-    return _scratch(need, x), True
 
 
 def _keep(t, stream):
@@ -218,6 +195,17 @@ def _ssd_state(state, nheads, headdim, dstate, device):
     return slots, ptr, stride
 
 
+def _ssd_packed(args, x, workspace, stream):
+    """The call with its device current; returns the workspace it used."""
+    status, used = _binding.ssd_packed(_address("mamba_ssd_packed_fwd"), _address("mamba_ssd_packed_workspace_size"),
+                                       _stream(x, stream), args, x, workspace)
+    if status:
+        raise MambaScanError(status, load_library().mamba_last_error().decode(errors="replace"))
+    if used is not workspace:
+        _keep(used, stream)
+    return used
+
+
 def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_softplus=True, state=None,
                    state_indices=None, has_initial_state=None, max_seqlen=0, out=None, workspace=None, check=True,
                    stream=None, wait_limit_us=0):
@@ -255,14 +243,13 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
         *_rows("B", B, dtype, bc, device), *_rows("C", C, dtype, bc, device), *_rows("z", z, dtype, shape, device),
         *_rows("out", y, dtype, shape, device), _vector("A", A, nheads, device, _F32), _vector("D", D, nheads, device, _F32),
         _vector("dt_bias", dt_bias, nheads, device, _F32), st, slot_stride, cu, idx, flags, int(wait_limit_us), 0)
-    need = _workspace_bytes(device, "mamba_ssd_packed_workspace_size", args)
-    workspace, own = _workspace(x, workspace, need)
-    _run(device, stream, _fn("mamba_ssd_packed_fwd", _str, _ptr, _size, _ptr), args, workspace.data_ptr(),
-         workspace.numel())
-    if own:
-        _keep(workspace, stream)
+    if device.index != _current_device():
+        with torch.cuda.device(device):
+            used = _ssd_packed(args, x, workspace, stream)
+    else:
+        used = _ssd_packed(args, x, workspace, stream)
     if check:
-        ssd_check(workspace, stream)
+        ssd_check(used, stream)
     return y
 
 
