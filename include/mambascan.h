@@ -693,7 +693,8 @@ ms_status mamba_ssd_packed_workspace_size(const ms_ssd_packed_args *args, size_t
  * Rounding: y is formed from operands rounded to bf16 once (the decay mask times
  * C B^T, and the state that C reads); the states stay float32, accurate to about
  * 2^-16 of the sum of the absolute values they are made of. One token's decay
- * exp(delta A) below 2^-160 counts as 2^-160. An infinity or NaN in x spreads
+ * exp(delta A) below 2^-160 counts as 2^-160; one that is NaN makes y NaN from
+ * its token on, and the state. An infinity or NaN in x spreads
  * over the rows of its head and chunk of 128 tokens (0 times it is added
  * there), and to the rows behind; other sequences are not touched.
  */

@@ -279,7 +279,13 @@ __device__ __forceinline__ float delta_of(const SsdPackedParams &p, uint16_t dt,
     return p.softplus ? softplus_fine(v) : v;
 }
 
-__device__ __forceinline__ float log2_decay(float delta, float A2) { return fmaxf(delta * A2, kMinStep); }
+// (max.NaN: a decay that is NaN stays NaN, which fmaxf would replace by the bound)
+__device__ __forceinline__ float log2_decay(float delta, float A2)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(delta * A2), "f"(kMinStep));
+    return r;
+}
 
 // Exclusive suffix sums over 128 tokens, four per lane, and the sum of all, of two chunks.
 __device__ __forceinline__ void suffix_sums2(const float (&a)[2][4], int lane, float (&suf)[2][4], float (&all)[2])
