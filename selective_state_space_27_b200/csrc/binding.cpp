@@ -6,7 +6,7 @@
 //   vector(name, t, n, device, dtype)   -> pointer
 //   empty_like(t)                       -> an uninitialised tensor like it
 //   norm_fwd(entry point, stream, arguments of serving.norm_fwd) -> (status, y, residual_out)
-//   norm_bwd(entry point, its workspace query, stream, arguments) -> (status, dx, dz, dresidual, dweight, scratch)
+//   norm_bwd(entry point, its workspace query, stream, arguments) -> (status, dx, dz, dresidual, dweight)
 //   ssd_packed(entry point, its workspace query, stream, packed arguments, x, workspace) -> (status, workspace used)
 // A None tensor has pointer and stride 0; what does not fit raises ValueError or,
 // for a type, TypeError.
@@ -322,11 +322,11 @@ PyObject *norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
             status = fn(&p, &g, space, bytes, stream);
             Py_END_ALLOW_THREADS
         }
-        PyObject *r = PyTuple_New(6);
+        PyObject *r = PyTuple_New(5);
         if (!r) return nullptr;
         PyTuple_SET_ITEM(r, 0, PyLong_FromLong(status));
-        const at::Tensor *results[] = {&dx, &dz, &dres, &dw, &scratch};
-        for (int i = 0; i < 5; ++i)
+        const at::Tensor *results[] = {&dx, &dz, &dres, &dw};
+        for (int i = 0; i < 4; ++i)
             PyTuple_SET_ITEM(r, i + 1, results[i]->defined() ? THPVariable_Wrap(*results[i]) : Py_NewRef(Py_None));
         return r;
     } catch (const Refused &r) {

@@ -6,6 +6,11 @@ compiled ``_binding`` (``csrc/binding.cpp``), and their pointers and strides pac
 into the C structs of ``include/mambascan.h`` with :mod:`struct` (the norms' in the
 compiled module); the structs' ctypes mirrors (``ConvPackedArgs`` and so on) describe
 the same layouts. Outputs are allocated by the call unless ``out`` is given.
+
+``stream``: the torch.cuda.Stream that the call runs on, in place of the current one, as
+in a ``with torch.cuda.stream(stream)`` block: its scratch and outputs are that stream's.
+Ordering it against the streams that make the inputs and read the outputs, and keeping the
+inputs until it is done with them, is the caller's part.
 """
 from __future__ import annotations
 
@@ -58,10 +63,29 @@ def _address(name):
     return a
 
 
-def _stream(x, stream):
-    """Handle of ``stream`` or of the current stream of x's device."""
-    if stream is not None:
-        return stream.cuda_stream
+def _given(stream, x, call, *args):
+    """``call(*args)`` with ``stream`` current, for the calls that are given one.
+
+    Their scratch and outputs are then allocated from that stream's memory. From the
+    caller's stream they could get memory that work still running there uses, or,
+    dropped by the caller, give it up while ``stream`` still writes it. The outputs
+    are marked as used by the caller's stream too, where they are read.
+    """
+    if not x.is_cuda:
+        return call(*args)   # (refuses x)
+    if stream.device != x.device:
+        raise ValueError(f"stream is on {stream.device}, expected {x.device}")
+    caller = torch.cuda.current_stream(x.device)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(caller)
+    return out
+
+
+def _stream(x):
+    """Handle of the current stream of x's device."""
     if not x.is_cuda:
         return 0
     if _raw_stream is not None:
@@ -72,26 +96,18 @@ def _stream(x, stream):
 _str, _ptr = ctypes.c_char_p, ctypes.c_void_p
 
 
-def _run(device, stream, fn, *args):
-    """``fn(*args, stream)`` with ``device`` current, on ``stream`` or the device's current stream."""
+def _run(device, fn, *args):
+    """``fn(*args, stream)`` with ``device`` current, on its current stream."""
     if device.index != _current_device():
         with torch.cuda.device(device):
-            return _run(device, stream, fn, *args)
-    if stream is not None:
-        s = stream.cuda_stream
-    elif _raw_stream is not None:
+            return _run(device, fn, *args)
+    if _raw_stream is not None:
         s = _raw_stream(device.index)
     else:
         s = torch.cuda.current_stream(device).cuda_stream
     status = fn(*args, s)
     if status:
         raise MambaScanError(status, load_library().mamba_last_error().decode(errors="replace"))
-
-
-def _keep(t, stream):
-    """Scratch allocated on the current stream but used on ``stream``."""
-    if stream is not None:
-        t.record_stream(stream)
 
 
 def _cuda(x, ndim, what):
@@ -126,6 +142,8 @@ def _offsets(cu_seqlens, device):
 # ---- convolution ---------------------------------------------------------------
 
 def _conv(x, weight, bias, silu, cu, nseq, state, state_indices, has_initial_state, out, stream):
+    if stream is not None:
+        return _given(stream, x, _conv, x, weight, bias, silu, cu, nseq, state, state_indices, has_initial_state, out, None)
     device, code = _cuda(x, 2, "x")
     tokens, channels = shape = x.shape
     y = _empty_like(x) if out is None else out
@@ -152,7 +170,7 @@ def _conv(x, weight, bias, silu, cu, nseq, state, state_indices, has_initial_sta
     args = CONV_PACKED.pack(tokens, channels, nseq, slots, code, 0, xp, xs, yp, ys, st, slot_stride, row_stride,
                             cu, idx, flags)
     conv = CONV1D.pack(wp, _vector("conv bias", bias, channels, device, _F32), width, 1 if silu else 0)
-    _run(device, stream, _fn("mamba_conv_packed_fwd", _str, _str, _ptr), args, conv)
+    _run(device, _fn("mamba_conv_packed_fwd", _str, _str, _ptr), args, conv)
     return y
 
 
@@ -195,14 +213,12 @@ def _ssd_state(state, nheads, headdim, dstate, device):
     return slots, ptr, stride
 
 
-def _ssd_packed(args, x, workspace, stream):
+def _ssd_packed(args, x, workspace):
     """The call with its device current; returns the workspace it used."""
     status, used = _binding.ssd_packed(_address("mamba_ssd_packed_fwd"), _address("mamba_ssd_packed_workspace_size"),
-                                       _stream(x, stream), args, x, workspace)
+                                       _stream(x), args, x, workspace)
     if status:
         raise MambaScanError(status, load_library().mamba_last_error().decode(errors="replace"))
-    if used is not workspace:
-        _keep(used, stream)
     return used
 
 
@@ -225,6 +241,9 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
     kernel reported a failed wait; without it, pass a workspace and call
     :func:`ssd_check` on it later.
     """
+    if stream is not None:
+        return _given(stream, x, ssd_packed_fwd, x, dt, A, B, C, cu_seqlens, D, z, dt_bias, dt_softplus, state, state_indices,
+                      has_initial_state, max_seqlen, out, workspace, check, None, wait_limit_us)
     device, code = _cuda(x, 3, "x")
     dtype = x.dtype
     tokens, nheads, headdim = shape = x.shape
@@ -245,11 +264,11 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
         _vector("dt_bias", dt_bias, nheads, device, _F32), st, slot_stride, cu, idx, flags, int(wait_limit_us), 0)
     if device.index != _current_device():
         with torch.cuda.device(device):
-            used = _ssd_packed(args, x, workspace, stream)
+            used = _ssd_packed(args, x, workspace)
     else:
-        used = _ssd_packed(args, x, workspace, stream)
+        used = _ssd_packed(args, x, workspace)
     if check:
-        ssd_check(used, stream)
+        ssd_check(used)
     return y
 
 
@@ -265,6 +284,8 @@ def ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_sof
     nheads, headdim); rows whose index lies outside the cache, or is an earlier
     row's, are skipped (output row and cache stay as they were).
     """
+    if stream is not None:
+        return _given(stream, x, ssd_state_update, state, x, dt, A, B, C, D, z, dt_bias, dt_softplus, state_indices, out)
     device, code = _cuda(x, 3, "x")
     dtype = x.dtype
     batch, nheads, headdim = shape = x.shape
@@ -279,7 +300,7 @@ def ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_sof
         *_rows("B", B, dtype, bc, device), *_rows("C", C, dtype, bc, device), *_rows("z", z, dtype, shape, device),
         *_rows("out", y, dtype, shape, device), _vector("A", A, nheads, device, _F32), _vector("D", D, nheads, device, _F32),
         _vector("dt_bias", dt_bias, nheads, device, _F32), _vector("state_indices", state_indices, batch, device, torch.int32))
-    _run(device, stream, _fn("mamba_ssd_state_update", _str, _ptr), args)
+    _run(device, _fn("mamba_ssd_state_update", _str, _ptr), args)
     return y
 
 
@@ -296,10 +317,13 @@ def norm_fwd(x, weight=None, z=None, residual=None, residual_scale=1.0, eps=1e-5
     rows of any stride; weight (dim,) float32 or None. Returns ``(y,
     residual_out)``, residual_out None without a residual.
     """
+    if stream is not None:
+        return _given(stream, x, norm_fwd, x, weight, z, residual, residual_scale, eps, group_size, gate_first, out,
+                      residual_out)
     if x.is_cuda and x.device.index != _current_device():
         with torch.cuda.device(x.device):
-            return norm_fwd(x, weight, z, residual, residual_scale, eps, group_size, gate_first, out, residual_out, stream)
-    status, y, total = _binding.norm_fwd(_address("mamba_norm_fwd"), _stream(x, stream), x, weight, z, residual,
+            return norm_fwd(x, weight, z, residual, residual_scale, eps, group_size, gate_first, out, residual_out)
+    status, y, total = _binding.norm_fwd(_address("mamba_norm_fwd"), _stream(x), x, weight, z, residual,
                                          residual_scale, eps, group_size, gate_first, out, residual_out)
     if status:
         raise MambaScanError(status, load_library().mamba_last_error().decode(errors="replace"))
@@ -316,15 +340,16 @@ def norm_bwd(dy, x, weight=None, z=None, residual_out=None, dresidual_out=None, 
     in the residual's, dweight (dim,) float32 (None without weight).
     ``workspace``: optional uint8 CUDA tensor, allocated here when needed.
     """
+    if stream is not None:
+        return _given(stream, x, norm_bwd, dy, x, weight, z, residual_out, dresidual_out, residual_scale, eps, group_size,
+                      gate_first, workspace)
     if x.is_cuda and x.device.index != _current_device():
         with torch.cuda.device(x.device):
             return norm_bwd(dy, x, weight, z, residual_out, dresidual_out, residual_scale, eps, group_size, gate_first,
-                            workspace, stream)
-    status, dx, dz, dresidual, dweight, scratch = _binding.norm_bwd(
-        _address("mamba_norm_bwd"), _address("mamba_norm_bwd_workspace_size"), _stream(x, stream), dy, x, weight, z,
+                            workspace)
+    status, dx, dz, dresidual, dweight = _binding.norm_bwd(
+        _address("mamba_norm_bwd"), _address("mamba_norm_bwd_workspace_size"), _stream(x), dy, x, weight, z,
         residual_out, dresidual_out, residual_scale, eps, group_size, gate_first, workspace)
     if status:
         raise MambaScanError(status, load_library().mamba_last_error().decode(errors="replace"))
-    if scratch is not None:
-        _keep(scratch, stream)
     return {"dx": dx, "dz": dz, "dresidual": dresidual, "dweight": dweight}

@@ -74,3 +74,116 @@ def test_nan_step_reaches_what_follows(ms, lens, H, longest, at):
     ssd_close(y[~hit], None, want[~hit], None, ymag[~hit], None)
     clean = ~torch.isnan(new)
     close(state[clean], new[clean], 2 * UB * UB * smag[clean])
+
+
+# ---- other streams --------------------------------------------------------------------
+
+def on_stream_calls(ms, g):
+    """name -> (call of a stream, shapes and types of what it allocates)."""
+    bf = torch.bfloat16
+    x, z, w = normal(g, 3000, 512, dtype=bf), normal(g, 3000, 512, dtype=bf), normal(g, 512)
+    res = normal(g, 3000, 512)
+    filt, conv_state = normal(g, 512, 4), normal(g, 3000, 3, 512, dtype=bf)
+    a, kw, _ = ssd_inputs(g, 3000, 2, 1, False)
+    token = dict(zip(a, [t[:700] if t.dim() > 1 else t for t in a.values()]))
+    state = torch.zeros(700, 2, 64, 128, device="cuda")
+    cu = i32([0, 3000])
+    rows = ((3000, 512), bf)
+    kept = []
+
+    def fresh(cache):
+        kept.append(cache.clone())   # (of the current stream: kept, and there before another stream uses it)
+        torch.cuda.synchronize()
+        return kept[-1]
+
+    return {
+        "norm_fwd": (lambda s: ms.norm_fwd(x, weight=w, residual=res, stream=s), [rows, ((3000, 512), torch.float32)]),
+        "norm_bwd": (lambda s: ms.norm_bwd(x, x, weight=w, z=z, stream=s), [rows, rows, ((512,), torch.float32)]),
+        "conv_packed_fwd": (lambda s: ms.conv_packed_fwd(x, filt, cu, stream=s), [rows]),
+        "conv_packed_update": (lambda s: ms.conv_packed_update(fresh(conv_state), x, filt, stream=s), [rows]),
+        "ssd_packed_fwd": (lambda s: ms.ssd_packed_fwd(*a.values(), cu, stream=s, check=False, **kw),
+                           [((3000, 2, 64), bf), ((1 << 21,), torch.uint8)]),
+        "ssd_state_update": (lambda s: ms.ssd_state_update(fresh(state), *token.values(), stream=s, **kw),
+                             [((700, 2, 64), bf)]),
+    }
+
+
+def tensors(result):
+    return [t for t in (result.values() if isinstance(result, dict) else result if isinstance(result, tuple) else [result])
+            if t is not None]
+
+
+@pytest.mark.parametrize("name", ["norm_fwd", "norm_bwd", "conv_packed_fwd", "conv_packed_update", "ssd_packed_fwd",
+                                  "ssd_state_update"])
+def test_given_stream_owns_what_the_call_allocates(ms, name):
+    """With ``stream`` the outputs are not memory that the current stream has just given back (its work may still use
+    it), and memory of dropped outputs does not go to the current stream while the call still writes it."""
+    call, shapes = on_stream_calls(ms, rng(3))[name]
+    want = [t.clone() for t in tensors(call(None))]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    blocks = [torch.empty(s, dtype=t, device="cuda") for s, t in shapes for _ in range(3)]
+    freed = [(b.data_ptr(), b.data_ptr() + b.numel() * b.element_size()) for b in blocks]
+    del blocks
+    got = tensors(call(side))
+    assert len(got) == len(want)
+    assert not any(lo <= t.data_ptr() < hi for t in got for lo, hi in freed)
+    side.synchronize()
+    assert all(torch.equal(t, w) for t, w in zip(got, want))
+    for _ in range(5):
+        places = [t.data_ptr() for t in tensors(call(side))]      # dropped at once
+        mine = [torch.full_like(w, 3.0) for w in want]
+        assert not set(places) & {t.data_ptr() for t in mine}
+        torch.cuda.synchronize()
+        assert all((t == 3.0).all() for t in mine)
+
+
+def test_given_stream_beside_unchecked_calls_of_the_current_one(ms):
+    """A call in segments whose workspace is dropped while it runs, and one of the same size on another stream right
+    behind it: each keeps to its own workspace."""
+    g = rng(12)
+    work = [ssd_inputs(g, 16384, 4, 1, False)[:2] for _ in range(2)]
+    cu = i32([0, 16384])
+
+    def call(k, stream=None, check=False):
+        a, kw = work[k]
+        state = torch.zeros(1, 4, 64, 128, device="cuda")
+        y = ms.ssd_packed_fwd(*a.values(), cu, state=state, max_seqlen=16384, stream=stream, check=check, **kw)
+        return y, state
+
+    want = [call(k, check=True) for k in range(2)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    states = torch.zeros(2, 1, 4, 64, 128, device="cuda")
+    for _ in range(10):
+        states.zero_()
+        torch.cuda.synchronize()
+        out = []
+        for k, stream in ((0, None), (1, side)):
+            a, kw = work[k]
+            out.append(ms.ssd_packed_fwd(*a.values(), cu, state=states[k], max_seqlen=16384, stream=stream, check=False,
+                                         **kw))
+        torch.cuda.synchronize()
+        for k in range(2):
+            assert torch.equal(out[k], want[k][0]) and torch.equal(states[k], want[k][1])
+
+
+def test_stream_of_the_inputs_device(ms):
+    """``stream`` positional, as keyword, in a capture; with host tensors the tensor is refused."""
+    g = rng(4)
+    x, w = normal(g, 40, 64), normal(g, 64)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want = ms.norm_fwd(x, weight=w)[0]
+    graph = torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        y, _ = ms.norm_fwd(x, weight=w, stream=side)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    with pytest.raises(ValueError, match="CUDA"):
+        ms.norm_fwd(x.cpu(), stream=side)
+    with pytest.raises(ValueError, match="CUDA"):
+        ms.conv_packed_update(x.cpu(), x.cpu(), w, stream=side)
