@@ -12,7 +12,9 @@ section "Como o Mamba-1 alcançou complexidade linear"):
   updated in place (decode).
 
 This module only marshals arguments: PyTorch supplies device memory and the
-current CUDA stream, and every step of the computation runs in the CUDA
+current CUDA stream (or the call's ``stream``, as in a ``with torch.cuda.stream(stream)``
+block: scratch and outputs are that stream's; ordering it against other streams is
+the caller's part), and every step of the computation runs in the CUDA
 kernels of ``libmambascan.so``. There is no CPU fallback: if the library is
 missing or cannot be loaded, every call raises.
 """
@@ -327,19 +329,35 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_ptr(stream):
+def _stream_ptr(stream=None):
     torch = _torch()
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
 
-def _keep_until_done(t, stream):
-    """A scratch tensor allocated here on the current stream but used by a
-    launch on ``stream``: tell the caching allocator not to hand its memory to
-    other work before that stream has finished with it."""
-    if stream is not None:
-        t.record_stream(stream)
+def _given(stream, x, call, kw):
+    """``call(**kw)`` with ``stream`` current, for a call that was given one (x: the
+    tensor whose device it runs on).
+
+    Its scratch and outputs are then allocated from that stream's memory. From the
+    caller's stream they could get memory that work still running there uses, or,
+    dropped by the caller, give it up while ``stream`` still writes it. The outputs
+    are marked as used by the caller's stream too, where they are read.
+    """
+    torch = _torch()
+    kw["stream"] = None
+    if not x.is_cuda:
+        return call(**kw)   # (refuses x)
+    if stream.device != x.device:
+        raise ValueError(f"stream is on {stream.device}, expected {x.device}")
+    caller = torch.cuda.current_stream(x.device)
+    with torch.cuda.stream(stream):
+        out = call(**kw)
+    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(caller)
+    return out
 
 
 def _need_cuda(name, t, dtype=None, ndim=None):
@@ -458,6 +476,8 @@ def scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta_softplus=
     receives the state after every 8th step, for :func:`scan_bwd` (automatic
     plan only).
     """
+    if stream is not None:
+        return _given(stream, u, scan_fwd, locals())
     torch = _torch()
     y = torch.empty_like(u) if out is None else out
     hT = None
@@ -472,11 +492,10 @@ def scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta_softplus=
             need = scan_workspace_size(args)
         else:
             need = plan_workspace_size(args, plan)
-        ws_ptr, ws_bytes, own_ws = None, 0, False
+        ws_ptr, ws_bytes = None, 0
         if need:
             if workspace is None or workspace.numel() < need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=u.device)
-                own_ws = True
             ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
         if checkpoints is not None:
             if plan is not None:
@@ -485,14 +504,12 @@ def scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta_softplus=
             if not checkpoints.is_contiguous():
                 raise ValueError("checkpoints must be contiguous")
             _check(lib.mamba_scan_fwd_checkpointed(ctypes.byref(args), checkpoints.data_ptr(),
-                                                   checkpoints.numel() * 4, ws_ptr, ws_bytes, _stream_ptr(stream)))
+                                                   checkpoints.numel() * 4, ws_ptr, ws_bytes, _stream_ptr()))
         elif plan is None:
-            _check(lib.mamba_scan_fwd(ctypes.byref(args), ws_ptr, ws_bytes, _stream_ptr(stream)))
+            _check(lib.mamba_scan_fwd(ctypes.byref(args), ws_ptr, ws_bytes, _stream_ptr()))
         else:
             _check(lib.mamba_scan_fwd_with_plan(ctypes.byref(args), ctypes.byref(plan), ws_ptr, ws_bytes,
-                                                _stream_ptr(stream)))
-        if own_ws:
-            _keep_until_done(workspace, stream)
+                                                _stream_ptr()))
     return (y, hT) if return_last_state else y
 
 
@@ -539,12 +556,14 @@ def build_update_args(state, x, delta, A, B, C, y, *, D=None, z=None, delta_bias
 def state_update(state, x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_softplus=True,
                  out=None, stream=None):
     """One decode step: updates ``state`` (batch, dim, dstate) float32 in place; returns y (batch, dim)."""
+    if stream is not None:
+        return _given(stream, x, state_update, locals())
     torch = _torch()
     y = torch.empty_like(x) if out is None else out
     args = build_update_args(state, x, delta, A, B, C, y, D=D, z=z, delta_bias=delta_bias,
                              delta_softplus=delta_softplus)
     with torch.cuda.device(x.device):
-        _check(load_library().mamba_state_update(ctypes.byref(args), _stream_ptr(stream)))
+        _check(load_library().mamba_state_update(ctypes.byref(args), _stream_ptr()))
     return y
 
 
@@ -572,6 +591,8 @@ def conv_scan_fwd(x, conv_weight, delta, A, B, C, D=None, z=None, delta_bias=Non
     u = silu(conv(x)). Other arguments as :func:`scan_fwd` (no segments);
     ``plan`` may ask for the persistent schedule (ctas > 0), whose workspace
     is allocated here."""
+    if stream is not None:
+        return _given(stream, x, conv_scan_fwd, locals())
     torch = _torch()
     y = torch.empty_like(x) if out is None else out
     hT = None
@@ -590,9 +611,7 @@ def conv_scan_fwd(x, conv_weight, delta, A, B, C, D=None, z=None, delta_bias=Non
         workspace = torch.empty(n.value, dtype=torch.uint8, device=x.device) if n.value else None
         _check(lib.mamba_conv_scan_fwd_ws(ctypes.byref(args), ctypes.byref(conv), plan_ref,
                                           None if workspace is None else workspace.data_ptr(), n.value,
-                                          _stream_ptr(stream)))
-        if workspace is not None:
-            _keep_until_done(workspace, stream)
+                                          _stream_ptr()))
     return (y, hT) if return_last_state else y
 
 
@@ -601,6 +620,8 @@ def conv_state_update(state, conv_state, x, conv_weight, delta, A, B, C, D=None,
     """One decode step with the convolution prologue: ``conv_state`` (batch,
     dim, width) in x's dtype holds the last ``width`` inputs (oldest first) and
     is updated in place with ``x``; ``state`` as :func:`state_update`."""
+    if stream is not None:
+        return _given(stream, x, conv_state_update, locals())
     torch = _torch()
     y = torch.empty_like(x) if out is None else out
     args = build_update_args(state, x, delta, A, B, C, y, D=D, z=z, delta_bias=delta_bias,
@@ -612,7 +633,7 @@ def conv_state_update(state, conv_state, x, conv_weight, delta, A, B, C, D=None,
     with torch.cuda.device(x.device):
         _check(load_library().mamba_conv_state_update(ctypes.byref(args), ctypes.byref(conv), _ptr(conv_state),
                                                       conv_state.stride(0), conv_state.stride(1),
-                                                      _stream_ptr(stream)))
+                                                      _stream_ptr()))
     return y
 
 
@@ -622,6 +643,8 @@ def trap_scan_fwd(u, delta, lambda_raw, A, B, C, D=None, z=None, delta_bias=None
     plus ``lambda_raw`` (batch, dim, L) in u's dtype, lambda = sigmoid(lambda_raw)
     mixing the previous and the current input (no segments); ``plan`` may ask
     for the persistent schedule (ctas > 0), whose workspace is allocated here."""
+    if stream is not None:
+        return _given(stream, u, trap_scan_fwd, locals())
     torch = _torch()
     _need_cuda("lambda_raw", lambda_raw, u.dtype, 3)
     if tuple(lambda_raw.shape) != tuple(u.shape):
@@ -641,9 +664,7 @@ def trap_scan_fwd(u, delta, lambda_raw, A, B, C, D=None, z=None, delta_bias=None
         workspace = torch.empty(n.value, dtype=torch.uint8, device=u.device) if n.value else None
         _check(lib.mamba_trap_scan_fwd_ws(ctypes.byref(args), *lam, plan_ref,
                                           None if workspace is None else workspace.data_ptr(), n.value,
-                                          _stream_ptr(stream)))
-        if workspace is not None:
-            _keep_until_done(workspace, stream)
+                                          _stream_ptr()))
     return (y, hT) if return_last_state else y
 
 
@@ -667,6 +688,8 @@ def scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, delta_softp
     filled; the backward then recomputes from it instead of sweeping the
     sequence forward first.
     """
+    if stream is not None:
+        return _given(stream, u, scan_bwd, locals())
     torch = _torch()
     batch, dim, L = u.shape
     N = B.shape[1]
@@ -704,17 +727,14 @@ def scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, delta_softp
             if not checkpoints.is_contiguous():
                 raise ValueError("checkpoints must be contiguous")
             _check(lib.mamba_scan_bwd_checkpointed(ctypes.byref(args), ctypes.byref(g), checkpoints.data_ptr(),
-                                                   checkpoints.numel() * 4, _stream_ptr(stream)))
+                                                   checkpoints.numel() * 4, _stream_ptr()))
             return out
         n = ctypes.c_size_t(0)
         _check(lib.mamba_scan_bwd_workspace_size(ctypes.byref(args), ctypes.byref(n)))
-        own_ws = workspace is None or workspace.numel() < n.value
-        if own_ws:
+        if workspace is None or workspace.numel() < n.value:
             workspace = torch.empty(max(n.value, 1), dtype=torch.uint8, device=u.device)
         _check(lib.mamba_scan_bwd(ctypes.byref(args), ctypes.byref(g), workspace.data_ptr(), workspace.numel(),
-                                  _stream_ptr(stream)))
-        if own_ws:
-            _keep_until_done(workspace, stream)
+                                  _stream_ptr()))
     return out
 
 
@@ -790,6 +810,8 @@ def ssd_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, init
     of the kernel's pipeline waits (0: about one second); ``withhold_block``
     is the fault-injection hook of ``ms_ssd_args`` (tests only).
     """
+    if stream is not None:
+        return _given(stream, x, ssd_fwd, locals())
     torch = _torch()
     y = torch.empty_like(x) if out is None else out
     hT = None
@@ -799,18 +821,15 @@ def ssd_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, init
                           initial_state=initial_state, final_state=hT)
     args.wait_limit_us = int(wait_limit_us)
     args.withhold_block = int(withhold_block)
-    own_ws = workspace is None
     lib = load_library()
     with torch.cuda.device(x.device):
-        if own_ws:
+        if workspace is None:
             n = ctypes.c_size_t(0)
             _check(lib.mamba_ssd_workspace_size(ctypes.byref(args), ctypes.byref(n)))
             workspace = torch.empty(n.value, dtype=torch.uint8, device=x.device)
-        _check(lib.mamba_ssd_fwd(ctypes.byref(args), workspace.data_ptr(), workspace.numel(), _stream_ptr(stream)))
-        if own_ws:
-            _keep_until_done(workspace, stream)
+        _check(lib.mamba_ssd_fwd(ctypes.byref(args), workspace.data_ptr(), workspace.numel(), _stream_ptr()))
     if check:
-        ssd_check(workspace, stream)
+        ssd_check(workspace)
     return y, hT
 
 

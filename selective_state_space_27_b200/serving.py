@@ -19,7 +19,7 @@ import struct
 
 import torch
 
-from . import (MS_BF16, MS_F32, SSD_DSTATE, SSD_HEADDIM, MambaScanError, load_library, ssd_check)
+from . import MS_BF16, MS_F32, SSD_DSTATE, SSD_HEADDIM, MambaScanError, _given, load_library, ssd_check
 
 try:
     from . import _binding
@@ -61,27 +61,6 @@ def _address(name):
     if a is None:
         a = _addresses[name] = ctypes.cast(load_library()[name], ctypes.c_void_p).value
     return a
-
-
-def _given(stream, x, call, *args):
-    """``call(*args)`` with ``stream`` current, for the calls that are given one.
-
-    Their scratch and outputs are then allocated from that stream's memory. From the
-    caller's stream they could get memory that work still running there uses, or,
-    dropped by the caller, give it up while ``stream`` still writes it. The outputs
-    are marked as used by the caller's stream too, where they are read.
-    """
-    if not x.is_cuda:
-        return call(*args)   # (refuses x)
-    if stream.device != x.device:
-        raise ValueError(f"stream is on {stream.device}, expected {x.device}")
-    caller = torch.cuda.current_stream(x.device)
-    with torch.cuda.stream(stream):
-        out = call(*args)
-    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
-        if t is not None:
-            t.record_stream(caller)
-    return out
 
 
 def _stream(x):
@@ -143,7 +122,7 @@ def _offsets(cu_seqlens, device):
 
 def _conv(x, weight, bias, silu, cu, nseq, state, state_indices, has_initial_state, out, stream):
     if stream is not None:
-        return _given(stream, x, _conv, x, weight, bias, silu, cu, nseq, state, state_indices, has_initial_state, out, None)
+        return _given(stream, x, _conv, locals())
     device, code = _cuda(x, 2, "x")
     tokens, channels = shape = x.shape
     y = _empty_like(x) if out is None else out
@@ -242,8 +221,7 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
     :func:`ssd_check` on it later.
     """
     if stream is not None:
-        return _given(stream, x, ssd_packed_fwd, x, dt, A, B, C, cu_seqlens, D, z, dt_bias, dt_softplus, state, state_indices,
-                      has_initial_state, max_seqlen, out, workspace, check, None, wait_limit_us)
+        return _given(stream, x, ssd_packed_fwd, locals())
     device, code = _cuda(x, 3, "x")
     dtype = x.dtype
     tokens, nheads, headdim = shape = x.shape
@@ -285,7 +263,7 @@ def ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_sof
     row's, are skipped (output row and cache stay as they were).
     """
     if stream is not None:
-        return _given(stream, x, ssd_state_update, state, x, dt, A, B, C, D, z, dt_bias, dt_softplus, state_indices, out)
+        return _given(stream, x, ssd_state_update, locals())
     device, code = _cuda(x, 3, "x")
     dtype = x.dtype
     batch, nheads, headdim = shape = x.shape
@@ -318,8 +296,7 @@ def norm_fwd(x, weight=None, z=None, residual=None, residual_scale=1.0, eps=1e-5
     residual_out)``, residual_out None without a residual.
     """
     if stream is not None:
-        return _given(stream, x, norm_fwd, x, weight, z, residual, residual_scale, eps, group_size, gate_first, out,
-                      residual_out)
+        return _given(stream, x, norm_fwd, locals())
     if x.is_cuda and x.device.index != _current_device():
         with torch.cuda.device(x.device):
             return norm_fwd(x, weight, z, residual, residual_scale, eps, group_size, gate_first, out, residual_out)
@@ -341,8 +318,7 @@ def norm_bwd(dy, x, weight=None, z=None, residual_out=None, dresidual_out=None, 
     ``workspace``: optional uint8 CUDA tensor, allocated here when needed.
     """
     if stream is not None:
-        return _given(stream, x, norm_bwd, dy, x, weight, z, residual_out, dresidual_out, residual_scale, eps, group_size,
-                      gate_first, workspace)
+        return _given(stream, x, norm_bwd, locals())
     if x.is_cuda and x.device.index != _current_device():
         with torch.cuda.device(x.device):
             return norm_bwd(dy, x, weight, z, residual_out, dresidual_out, residual_scale, eps, group_size, gate_first,
