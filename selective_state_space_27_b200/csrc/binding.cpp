@@ -7,7 +7,7 @@
 //   empty_like(t)                       -> an uninitialised tensor like it
 //   norm_fwd(entry point, stream, arguments of serving.norm_fwd) -> (status, y, residual_out)
 //   norm_bwd(entry point, its workspace query, stream, arguments) -> (status, dx, dz, dresidual, dweight)
-//   ssd_packed(entry point, its workspace query, stream, packed arguments, x, workspace) -> (status, workspace used)
+//   ssd_packed(entry point, its workspace query, stream, packed arguments, x, workspace, replace) -> (status, workspace used)
 // A None tensor has pointer and stride 0; what does not fit raises ValueError or,
 // for a type, TypeError.
 #define PY_SSIZE_T_CLEAN
@@ -335,17 +335,19 @@ PyObject *norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// The workspace's size, a workspace of that size where none large enough is given, and the call.
+// The workspace's size, a workspace of that size where none is given or (replace) the given
+// one is too small, and the call. Without replace the call refuses one that is too small.
 PyObject *ssd_packed(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (!arguments(n, 6)) return nullptr;
+    if (!arguments(n, 7)) return nullptr;
     try {
         const auto fn = entry<ms_status (*)(const ms_ssd_packed_args *, void *, size_t, void *)>(a[0]);
         const auto query = entry<ms_status (*)(const ms_ssd_packed_args *, size_t *)>(a[1]);
         void *stream = PyLong_AsVoidPtr(a[2]);
         char *bytes = nullptr;
         Py_ssize_t length = 0;
-        if (PyBytes_AsStringAndSize(a[3], &bytes, &length) < 0 || PyErr_Occurred()) return nullptr;
+        const int replace = PyObject_IsTrue(a[6]);
+        if (replace < 0 || PyBytes_AsStringAndSize(a[3], &bytes, &length) < 0 || PyErr_Occurred()) return nullptr;
         const at::Tensor *x = optional("x", a[4]), *given = optional("workspace", a[5]);
         if (!x || length != sizeof(ms_ssd_packed_args)) throw Refused{PyExc_ValueError, "the packed arguments do not fit"};
         ms_ssd_packed_args p;
@@ -356,7 +358,7 @@ PyObject *ssd_packed(PyObject *, PyObject *const *a, Py_ssize_t n) {
         ms_status status = query(&p, &need);
         at::Tensor space;
         if (status == MS_OK) {
-            space = given && static_cast<size_t>(given->numel()) >= need
+            space = given && (!replace || static_cast<size_t>(given->numel()) >= need)
                         ? *given
                         : at::empty({static_cast<int64_t>(need)}, x->options().dtype(at::kByte));
             void *at = space.data_ptr();
@@ -388,7 +390,7 @@ PyMethodDef methods[] = {
      "norm_bwd(entry point, query, stream, dy, x, weight, z, residual_out, dresidual_out, scale, eps, group_size, "
      "gate_first, workspace)."},
     {"ssd_packed", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(ssd_packed)), METH_FASTCALL,
-     "ssd_packed(entry point, query, stream, packed arguments, x, workspace)."},
+     "ssd_packed(entry point, query, stream, packed arguments, x, workspace, replace)."},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -192,10 +192,10 @@ def _ssd_state(state, nheads, headdim, dstate, device):
     return slots, ptr, stride
 
 
-def _ssd_packed(args, x, workspace):
+def _ssd_packed(args, x, workspace, replace):
     """The call with its device current; returns the workspace it used."""
     status, used = _binding.ssd_packed(_address("mamba_ssd_packed_fwd"), _address("mamba_ssd_packed_workspace_size"),
-                                       _stream(x), args, x, workspace)
+                                       _stream(x), args, x, workspace, replace)
     if status:
         raise MambaScanError(status, load_library().mamba_last_error().decode(errors="replace"))
     return used
@@ -215,10 +215,11 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
     every sequence starts from zero and leaves no state). ``max_seqlen``: the
     longest sequence if the host knows it; it steers the schedule only.
     Returns y (tokens, nheads, 64); rows of no or of a skipped sequence are not
-    written. ``workspace``: a uint8 CUDA tensor, allocated here when None or too
-    small. With ``check`` the call synchronizes the stream and raises if the
-    kernel reported a failed wait; without it, pass a workspace and call
-    :func:`ssd_check` on it later.
+    written. ``workspace``: a uint8 CUDA tensor, allocated here when None. With
+    ``check`` the call synchronizes the stream and raises if the kernel
+    reported a failed wait (a workspace that is too small is then replaced);
+    without it, pass a workspace and call :func:`ssd_check` on it later (one
+    that is too small is refused: the status would not be in it).
     """
     if stream is not None:
         return _given(stream, x, ssd_packed_fwd, locals())
@@ -242,9 +243,9 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
         _vector("dt_bias", dt_bias, nheads, device, _F32), st, slot_stride, cu, idx, flags, int(wait_limit_us), 0)
     if device.index != _current_device():
         with torch.cuda.device(device):
-            used = _ssd_packed(args, x, workspace)
+            used = _ssd_packed(args, x, workspace, check)
     else:
-        used = _ssd_packed(args, x, workspace)
+        used = _ssd_packed(args, x, workspace, check)
     if check:
         ssd_check(used)
     return y

@@ -187,3 +187,26 @@ def test_stream_of_the_inputs_device(ms):
         ms.norm_fwd(x.cpu(), stream=side)
     with pytest.raises(ValueError, match="CUDA"):
         ms.conv_packed_update(x.cpu(), x.cpu(), w, stream=side)
+
+
+# ---- workspaces ------------------------------------------------------------------------
+
+def test_small_workspace_is_refused_where_its_status_is_read_later(ms):
+    """With check=False the caller reads the status from the workspace it gave: one that is too small is refused, not
+    replaced. With check=True the call reads the status itself."""
+    g = rng(14)
+    a, kw, _ = ssd_inputs(g, 6000, 2, 1, False)
+    cu = i32([0, 6000])
+    want = ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=6000, **kw)
+    small = torch.full((256,), 0xAB, dtype=torch.uint8, device="cuda")
+    out = torch.full_like(want, 5.0)
+    for ws in (small, small[:0]):
+        with pytest.raises(ms.MambaScanError) as e:
+            ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=6000, out=out, workspace=ws, check=False, **kw)
+        assert e.value.status == 6                               # MS_ERR_WORKSPACE
+    assert (out == 5.0).all() and (small == 0xAB).all()
+    assert torch.equal(ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=6000, workspace=small, **kw), want)
+    large = torch.full((1 << 24,), 0xAB, dtype=torch.uint8, device="cuda")
+    ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=6000, out=out, workspace=large, check=False, **kw)
+    ms.ssd_check(large)
+    assert torch.equal(out, want)
