@@ -702,6 +702,14 @@ ms_status mamba_ssd_packed_fwd(const ms_ssd_packed_args *args, void *workspace, 
                                void *stream);
 
 /*
+ * Synchronizes `stream` and returns how many failures the mamba_ssd_packed_fwd
+ * calls on the current device have recorded in their status words since the
+ * library was loaded: for callers that do not keep the workspaces. The count
+ * never falls. MS_ERR_INVALID_ARG for NULL; MS_ERR_CUDA.
+ */
+ms_status mamba_ssd_packed_failures(uint64_t *count, void *stream);
+
+/*
  * One token per request through the Mamba-2 recurrence, states in slots:
  *   x, z, y : (batch, nheads, headdim), dt : (batch, nheads),
  *   B, C    : (batch, ngroups, dstate); batch strides given, inner axes contiguous

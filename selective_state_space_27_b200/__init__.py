@@ -286,6 +286,8 @@ def load_library():
                                                         ctypes.POINTER(ctypes.c_size_t)]
         lib.mamba_ssd_packed_fwd.restype = ctypes.c_int
         lib.mamba_ssd_packed_fwd.argtypes = [ctypes.POINTER(SsdPackedArgs), _vp, ctypes.c_size_t, _vp]
+        lib.mamba_ssd_packed_failures.restype = ctypes.c_int
+        lib.mamba_ssd_packed_failures.argtypes = [ctypes.POINTER(ctypes.c_uint64), _vp]
         lib.mamba_norm_fwd.restype = ctypes.c_int
         lib.mamba_norm_fwd.argtypes = [ctypes.POINTER(NormArgs), _vp]
         lib.mamba_norm_bwd_workspace_size.restype = ctypes.c_int
@@ -785,10 +787,25 @@ def build_ssd_args(x, dt, A, B, C, y, *, D=None, z=None, dt_bias=None, dt_softpl
     return a
 
 
-def ssd_check(workspace, stream=None):
+_failures_seen = {}   # of each device, by ssd_check without a workspace
+
+
+def ssd_check(workspace=None, stream=None):
     """Synchronize ``stream`` and raise :class:`MambaScanError` if the SSD
-    kernel that used ``workspace`` reported a failed internal wait."""
+    kernel that used ``workspace`` reported a failed internal wait. Without a
+    workspace: if any :func:`ssd_packed_fwd` on the device (the stream's or the
+    current one) reported one since the last such check, also to its caller."""
     torch = _torch()
+    if workspace is None:
+        stream = stream or torch.cuda.current_stream()
+        count = ctypes.c_uint64(0)
+        with torch.cuda.device(stream.device):
+            _check(load_library().mamba_ssd_packed_failures(ctypes.byref(count), stream.cuda_stream))
+        before = _failures_seen.get(stream.device.index, 0)
+        _failures_seen[stream.device.index] = count.value
+        if count.value != before:
+            raise MambaScanError(5, "a packed SSD kernel reported a failed internal wait")   # MS_ERR_TIMEOUT
+        return
     (stream or torch.cuda.current_stream(workspace.device)).synchronize()
     code = int(workspace[:4].view(torch.int32)[0].item())
     if code != 0:

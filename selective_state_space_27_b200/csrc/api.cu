@@ -941,6 +941,14 @@ ms_status mamba_ssd_packed_fwd(const ms_ssd_packed_args *a, void *workspace, siz
     return e == cudaSuccess ? MS_OK : cuda_fail(e, "packed SSD launch");
 }
 
+ms_status mamba_ssd_packed_failures(uint64_t *count, void *stream) {
+    if (!count) return invalid("count is NULL");
+    unsigned long long n = 0;
+    const cudaError_t e = ms::ssd_packed_failures(&n, static_cast<cudaStream_t>(stream));
+    *count = n;
+    return e == cudaSuccess ? MS_OK : cuda_fail(e, "reading the count of failures");
+}
+
 // What the forward and the backward norm share.
 static ms_status check_norm(const ms_norm_args *a) {
     if (!a) return invalid("args is NULL");

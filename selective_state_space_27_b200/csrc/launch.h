@@ -298,6 +298,8 @@ int64_t ssd_packed_places(int64_t tokens, int64_t nseq, int seg_chunks);
 size_t ssd_packed_ws_bytes(int64_t tokens, int64_t nseq, int64_t nheads, int seg_chunks);
 void ssd_packed_bind(SsdPackedParams &p, void *ws);
 cudaError_t launch_ssd_packed(const SsdPackedParams &p, cudaStream_t stream);
+// Failures recorded on the current device so far, once the stream is done.
+cudaError_t ssd_packed_failures(unsigned long long *count, cudaStream_t stream);
 
 // Record the message that mamba_last_error() returns on this thread.
 void record_error(const char *fmt, ...);

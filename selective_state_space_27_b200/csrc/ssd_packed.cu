@@ -144,6 +144,10 @@ constexpr uint32_t kColG = 0, kColM = 128, kColY = 256, kColS = 384;   // M', Y 
 __device__ __forceinline__ int step_of(int k) { return k & (kSteps - 1); }
 __device__ __forceinline__ uint32_t step_phase(int k) { return (uint32_t)(k / kSteps) & 1u; }
 
+// Failures on this device since the library was loaded, for callers that keep no
+// workspace and so no status word. Nothing reads it but ssd_packed_failures.
+__device__ unsigned long long failures;
+
 // A bounded wait. When its limit runs out it records that in the status word and
 // raises the CTA's abort flag; from then on every wait of the CTA returns at once,
 // no more loads are issued and the other roles run to their end on what is there:
@@ -159,6 +163,7 @@ __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile i
         if (global_ns() - t0 > limit_ns) {
             wait_for_previous();   // (the status word was cleared, or a kernel's failure is in it)
             give_up(status, abort_flag);
+            atomicAdd(&failures, 1ull);
         }
 }
 
@@ -435,7 +440,10 @@ __device__ __forceinline__ bool setup(const SsdPackedParams &p, uint8_t *smem, u
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (base & 1023u) {
         wait_for_previous();
-        if (threadIdx.x == 0) atomicExch(p.status, (int)MS_ERR_ALIGNMENT);
+        if (threadIdx.x == 0) {
+            atomicExch(p.status, (int)MS_ERR_ALIGNMENT);
+            atomicAdd(&failures, 1ull);
+        }
         return false;
     }
     // (the same for every thread)
@@ -1179,6 +1187,12 @@ void ssd_packed_bind(SsdPackedParams &p, void *ws)
     const int64_t places = ssd_packed_places(p.tokens, p.nseq, p.seg_chunks);
     p.seg_decay = reinterpret_cast<float *>(static_cast<char *>(ws) + decay_offset());
     p.seg_states = reinterpret_cast<float *>(static_cast<char *>(ws) + states_offset(places, p.nheads));
+}
+
+cudaError_t ssd_packed_failures(unsigned long long *count, cudaStream_t stream)
+{
+    cudaError_t e = cudaMemcpyFromSymbolAsync(count, failures, sizeof(*count), 0, cudaMemcpyDeviceToHost, stream);
+    return e == cudaSuccess ? cudaStreamSynchronize(stream) : e;
 }
 
 cudaError_t launch_ssd_packed(const SsdPackedParams &p, cudaStream_t stream)

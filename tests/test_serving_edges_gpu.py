@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import serving_ref as ref
-from tests.test_serving_gpu import F64, UB, close, i32, normal, offsets, rng, ssd_close, ssd_inputs
+from tests.test_serving_gpu import UB, close, i32, normal, offsets, rng, ssd_close, ssd_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -210,3 +210,31 @@ def test_small_workspace_is_refused_where_its_status_is_read_later(ms):
     ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=6000, out=out, workspace=large, check=False, **kw)
     ms.ssd_check(large)
     assert torch.equal(out, want)
+
+
+def test_failed_wait_of_an_unchecked_call_leaves_a_trace(ms):
+    """check=False without a workspace: the status word goes with the scratch, the count of failures stays. (A limit of
+    a microsecond on chunks of two heads, as in the timeout test of test_serving_gpu.py.)"""
+    g = rng(47)
+    a, kw, _ = ssd_inputs(g, 8 * 1100, 64, 1, False)
+    cu = offsets([1100] * 8)[1]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    try:
+        ms.ssd_check()                   # what earlier calls left
+    except ms.MambaScanError:
+        pass
+    want = ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=1100, **kw)
+    ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=1100, check=False, **kw)
+    ms.ssd_check()
+    for k in range(300):
+        ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=1100, check=False, wait_limit_us=1, stream=side, **kw)
+        try:
+            ms.ssd_check(stream=side)
+        except ms.MambaScanError as e:
+            assert e.status == 5         # MS_ERR_TIMEOUT
+            break
+    else:
+        assert False, "no wait ran out"
+    assert torch.equal(ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=1100, **kw), want)
+    ms.ssd_check()
