@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *partial, flo
     float s = 0.f;
     if (c < dim) {
 #pragma unroll 4
-        for (int64_t i = k; i < slabs; i += 128) s += __ldg(partial + i * dim + c);
+        for (int64_t i = k; i < slabs; i += 128) s += __ldcg(partial + i * dim + c);   // (written while this kernel runs)
     }
     s += __shfl_xor_sync(0xffffffffu, s, 8);
     s += __shfl_xor_sync(0xffffffffu, s, 16);

@@ -238,3 +238,20 @@ def test_failed_wait_of_an_unchecked_call_leaves_a_trace(ms):
         assert False, "no wait ran out"
     assert torch.equal(ms.ssd_packed_fwd(*a.values(), cu, max_seqlen=1100, **kw), want)
     ms.ssd_check()
+
+
+def test_norm_bwd_calls_in_a_row_with_one_workspace(ms):
+    """The sum over the slabs starts beside the kernel that writes their shares, here over the shares of the call in
+    front: every call gets its own."""
+    g = rng(15)
+    w = normal(g, 1530)
+    calls = [(normal(g, 1500 + 40 * i, 1530), normal(g, 1500 + 40 * i, 1530)) for i in range(6)]
+    alone = [ms.norm_bwd(dy, x, weight=w)["dweight"].clone() for x, dy in calls]
+    ws = torch.full((1 << 24,), 0xFF, dtype=torch.uint8, device="cuda")     # (NaN)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [ms.norm_bwd(dy, x, weight=w, workspace=ws)["dweight"] for x, dy in calls]
+    for _ in range(20):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, alone))
