@@ -279,7 +279,20 @@ cudaError_t launch_t(const ConvPackedParams &p, int num_sms, cudaStream_t stream
     };
     // Four channels per thread where sizes, strides and pointers allow it, else one.
     if (ok(4)) return launch_w<T, 4>(p, num_sms, stream);
-    return launch_w<T, 1>(p, num_sms, stream);
+    // One channel each: at most as many at a time as a grid's 65535 blocks in y hold.
+    constexpr int64_t kMost = static_cast<int64_t>(65535) * kMaxThreads;
+    for (int64_t c = 0; c < p.channels; c += kMost) {
+        ConvPackedParams q = p;
+        q.channels = min64(p.channels - c, kMost);
+        q.x = static_cast<const T *>(p.x) + c;
+        q.y = static_cast<T *>(p.y) + c;
+        if (p.state) q.state = static_cast<T *>(p.state) + c;
+        q.weight = p.weight + c * p.width;
+        if (p.bias) q.bias = p.bias + c;
+        const cudaError_t e = launch_w<T, 1>(q, num_sms, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace

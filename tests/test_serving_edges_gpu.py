@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import serving_ref as ref
-from tests.test_serving_gpu import UB, close, i32, normal, offsets, rng, ssd_close, ssd_inputs
+from tests.test_serving_gpu import F64, UB, close, conv_tol, i32, normal, offsets, rng, ssd_close, ssd_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -255,3 +255,18 @@ def test_norm_bwd_calls_in_a_row_with_one_workspace(ms):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, alone))
+
+
+# ---- the convolution's largest channel counts ----------------------------------------------
+
+@pytest.mark.parametrize("channels", [65535 * 64, 65535 * 64 + 1, (1 << 22) - 1, 1 << 22])
+def test_conv_packed_most_channels(ms, channels):
+    """One channel per thread where the count is no multiple of four: more blocks of channels than a grid has in y."""
+    g = rng(16)
+    x, weight, bias = normal(g, 2, channels), normal(g, channels, 2), normal(g, channels)
+    state = normal(g, 1, 1, channels)
+    cu, cu_t = offsets([2])
+    want, new, mag = ref.conv(x, weight, cu, bias, True, state, None, [True], torch.zeros_like(x))
+    got = ms.conv_packed_fwd(x, weight, cu_t, bias=bias, state=state, has_initial_state=torch.tensor([True], device="cuda"))
+    close(got, want, conv_tol(mag, want, torch.float32, 2))
+    assert torch.equal(state.to(F64), new)
