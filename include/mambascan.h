@@ -630,7 +630,7 @@ ms_status mamba_scan_fwd_noalloc(const ms_scan_args *args, void *stream);
  *   state : (slots, width - 1, channels) in_dtype, updated in place; entry and
  *           row strides given. Unused (NULL) when width is 1.
  * cu_seqlens NULL is the single-token form: tokens == nseq, sequence s is row s.
- * y must not overlap x (a row is read again for the rows behind it and the state).
+ * y must not overlap x, refused (a row is read again for the rows behind it and the state).
  */
 typedef struct ms_conv_packed_args {
     int64_t tokens, channels, nseq, slots;
@@ -716,7 +716,7 @@ ms_status mamba_ssd_packed_failures(uint64_t *count, void *stream);
  *   state   : (slots, nheads, headdim, dstate) float32, updated in place; slot
  *             stride given, inner axes contiguous
  * Any headdim up to 65535, dstate up to MS_SSD_UPDATE_MAX_DSTATE; in_dtype f32
- * or bf16.
+ * or bf16. y may be x or z itself, but overlap no other input.
  */
 #define MS_SSD_UPDATE_MAX_DSTATE 256
 typedef struct ms_ssd_update_args {

@@ -6,6 +6,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <numeric>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -739,6 +740,19 @@ static int dtype_bytes(int dtype) { return dtype == MS_F32 ? 4 : dtype == MS_BF1
 // Rows of packed tensors and cache slots are counted in 32 bits on the device.
 static const int64_t kMaxRows = (int64_t(1) << 31) - 1;
 
+// Whether two tensors of `rows` rows of `width` elements of eb bytes share an element; row strides in elements.
+// Exact for one stride (and one row); with two, rows that lie apart only by their numbers count as shared.
+static bool rows_overlap(const void *a, int64_t sa, const void *b, int64_t sb, int64_t rows, int64_t width, int eb) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    const __int128 d = (static_cast<__int128>(pb) - static_cast<__int128>(pa)), last = rows - 1;
+    if (d >= (last * sa + width) * eb || -d >= (last * sb + width) * eb) return false;   // one behind the other
+    if (rows == 1) return true;
+    // where the rows begin, modulo what both strides are multiples of
+    const __int128 period = static_cast<__int128>(std::gcd(sa, sb)) * eb, w = static_cast<__int128>(width) * eb;
+    const __int128 r = ((d % period) + period) % period;
+    return r < w || period - r < w;
+}
+
 // The checks that the packed calls share: counts, the cache and its index table.
 static ms_status check_slots(int64_t nseq, int64_t slots, const void *state, const int32_t *idx,
                              const uint8_t *has_init, bool need_state) {
@@ -772,6 +786,9 @@ ms_status mamba_conv_packed_fwd(const ms_conv_packed_args *a, const ms_conv1d_ar
     if (a->x_token_stride < 0 || a->y_token_stride < a->channels ||
         (stateful && (a->state_slot_stride < 0 || a->state_row_stride < a->channels)))
         return invalid("strides must be non-negative and those of y and the state rows cover the channels");
+    if (a->tokens > 0 &&
+        rows_overlap(a->x, a->x_token_stride, a->y, a->y_token_stride, a->tokens, a->channels, eb))
+        return invalid("y must not overlap x");
     if (stateful && a->slots > 1 && a->state_slot_stride < a->state_row_stride * (c->width - 1))
         return invalid("the state's slot stride must cover its rows");
     if (!elem_aligned(a->x, eb) || !elem_aligned(a->y, eb) || (stateful && !elem_aligned(a->state, eb)) ||

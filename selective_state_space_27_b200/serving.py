@@ -167,7 +167,8 @@ def conv_packed_fwd(x, weight, cu_seqlens, bias=None, silu=True, state=None, sta
     continues from it where ``has_initial_state[s]`` (bool; None: nowhere).
     Sequences with an index outside the cache, or an earlier sequence's, are
     skipped: their rows of the output and the cache stay as they were. Returns
-    y (tokens, channels); rows of no sequence are not written.
+    y (tokens, channels); rows of no sequence are not written. ``out`` must not
+    overlap x (the same or other rows): x's rows are read again for later ones.
     """
     cu, nseq = _offsets(cu_seqlens, x.device)
     return _conv(x, weight, bias, silu, cu, nseq, state, state_indices, has_initial_state, out, stream)
@@ -215,7 +216,7 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
     every sequence starts from zero and leaves no state). ``max_seqlen``: the
     longest sequence if the host knows it; it steers the schedule only.
     Returns y (tokens, nheads, 64); rows of no or of a skipped sequence are not
-    written. ``workspace``: a uint8 CUDA tensor, allocated here when None. With
+    written. ``out`` may be x or z itself, but overlap no other input, nor them in part. ``workspace``: a uint8 CUDA tensor, allocated here when None. With
     ``check`` the call synchronizes the stream and raises if the kernel
     reported a failed wait (a workspace that is too small is then replaced);
     without it, pass a workspace and call :func:`ssd_check` on it later (one
@@ -262,7 +263,8 @@ def ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_sof
     all bfloat16, the axes behind the batch contiguous; A, D, dt_bias
     (nheads,) float32. Any headdim, dstate up to 256. Returns y (batch,
     nheads, headdim); rows whose index lies outside the cache, or is an earlier
-    row's, are skipped (output row and cache stay as they were).
+    row's, are skipped (output row and cache stay as they were). ``out`` may be
+    x or z itself, but overlap no other input.
     """
     if stream is not None:
         return _given(stream, x, ssd_state_update, locals())
@@ -295,7 +297,8 @@ def norm_fwd(x, weight=None, z=None, residual=None, residual_scale=1.0, eps=1e-5
     dtype, x's or float32); y = v / sqrt(mean(v^2) + eps) * weight, times
     silu(z) when the gate comes last. x, z (rows, dim) float32 or bfloat16,
     rows of any stride; weight (dim,) float32 or None. Returns ``(y,
-    residual_out)``, residual_out None without a residual.
+    residual_out)``, residual_out None without a residual. ``out`` may be x or
+    z itself and ``residual_out`` residual; they overlap no other input.
     """
     if stream is not None:
         return _given(stream, x, norm_fwd, locals())

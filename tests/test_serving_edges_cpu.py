@@ -5,6 +5,7 @@ import pytest
 
 import selective_state_space_27_b200 as ms
 from selective_state_space_27_b200 import build as msbuild
+from tests.test_serving_cpu import BASE, conv_args, conv_filter
 
 
 @pytest.fixture(scope="module")
@@ -15,3 +16,16 @@ def lib():
 
 def test_failures_need_a_count(lib):
     assert lib.mamba_ssd_packed_failures(None, None) == 1
+
+
+@pytest.mark.parametrize("change", [
+    dict(y=BASE + 128), dict(y=BASE - 128), dict(y=BASE + 99 * 128 + 64),                     # later and earlier rows
+    dict(y=BASE + 126), dict(y=BASE - 2), dict(y=BASE + 2),                                   # an element of a row
+    dict(x_token_stride=200, y_token_stride=200, y=BASE + 126), dict(x_token_stride=200, y_token_stride=200, y=BASE + 274),
+    dict(x_token_stride=200, y_token_stride=100, y=BASE + 128), dict(x_token_stride=0, y=BASE - 64 * 128),
+    dict(tokens=1, y=BASE + 2), dict(tokens=1, y=BASE - 126),
+])
+def test_conv_packed_refuses_overlapping_outputs(lib, change):
+    """y that shares elements with x: its rows are written while x's are read again for later rows."""
+    assert lib.mamba_conv_packed_fwd(ctypes.byref(conv_args(**change)), ctypes.byref(conv_filter()), None) == 1
+    assert b"overlap" in lib.mamba_last_error()

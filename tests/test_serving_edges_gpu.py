@@ -270,3 +270,32 @@ def test_conv_packed_most_channels(ms, channels):
     got = ms.conv_packed_fwd(x, weight, cu_t, bias=bias, state=state, has_initial_state=torch.tensor([True], device="cuda"))
     close(got, want, conv_tol(mag, want, torch.float32, 2))
     assert torch.equal(state.to(F64), new)
+
+
+@pytest.mark.parametrize("where", ["columns", "columns_and_steps", "rows", "one_row"])
+def test_conv_packed_beside_its_input(ms, where):
+    """x and y in one buffer without a shared element: columns of the same rows, rows in turn, one behind the other."""
+    g = rng(17)
+    buf = normal(g, 120, 100)
+    x, out = {"columns": (buf[:60, :40], buf[:60, 40:80]), "columns_and_steps": (buf[::2, :40], buf[:60, 60:]),
+              "rows": (buf[::2, :40], buf[1::2, :40]), "one_row": (buf[:1, :40], buf[:1, 40:80])}[where]
+    weight = normal(g, 40, 4)
+    cu, cu_t = offsets([len(x)])
+    want, _, mag = ref.conv(x, weight, cu, None, True, None, None, None, torch.zeros(len(x), 40, device="cuda"))
+    close(ms.conv_packed_fwd(x, weight, cu_t, out=out), want, conv_tol(mag, want, torch.float32, 4))
+    with pytest.raises(ms.MambaScanError, match="overlap"):
+        ms.conv_packed_fwd(x, weight, cu_t, out=buf[:len(x), 30:70])
+
+
+@pytest.mark.parametrize("P,N,dtype", [(64, 128, torch.bfloat16), (7, 37, torch.float32), (48, 16, torch.float32)])
+def test_ssd_state_update_in_place(ms, P, N, dtype):
+    """y in the place of x, and of z."""
+    g = rng(P)
+    x, z = normal(g, 5, 2, P, dtype=dtype), normal(g, 5, 2, P, dtype=dtype)
+    B, C, dt = normal(g, 5, 1, N, dtype=dtype), normal(g, 5, 1, N, dtype=dtype), normal(g, 5, 2, dtype=dtype)
+    A, state = -torch.rand(2, device="cuda", generator=g), normal(g, 5, 2, P, N)
+    want = ms.ssd_state_update(state.clone(), x, dt, A, B, C, z=z)
+    for name in ("x", "z"):
+        c = dict(x=x.clone(), z=z.clone())
+        got = ms.ssd_state_update(state.clone(), c["x"], dt, A, B, C, z=c["z"], out=c[name])
+        assert got is c[name] and torch.equal(got, want)
