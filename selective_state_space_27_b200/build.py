@@ -71,11 +71,24 @@ def build_binding(verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every CUDA source for sm_100a into the in-tree shared library, and the binding."""
+    """Compile every CUDA source for sm_100a into the in-tree shared library, and, where
+    torch is installed, the binding. Returns the library's path."""
+    if force or not up_to_date():
+        build_library(verbose, ptxas_info)
+    try:
+        import torch   # noqa: F401
+    except ModuleNotFoundError as e:
+        if e.name != "torch":
+            raise
+        print("torch is not installed: only the CUDA library was built, not the Python calls' tensor checks", flush=True)
+        return LIB
     if force or not binding_up_to_date():
         build_binding(verbose)
-    if not force and up_to_date():
-        return LIB
+    return LIB
+
+
+def build_library(verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Compile every CUDA source for sm_100a into the in-tree shared library."""
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
     common = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
