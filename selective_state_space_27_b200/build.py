@@ -19,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmambascan.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_FOR = os.path.join(PKG, "_build", "binding_built_for")   # the torch and Python it was compiled against
 SOURCES = ["api.cu", "scan_fwd.cu", "scan_rec.cu", "scan_bwd.cu", "state_update.cu", "noalloc.cu", "ssd_fwd.cu", "probe.cu",
            "conv_packed.cu", "ssd_update.cu", "norm.cu", "ssd_packed.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -42,7 +43,20 @@ def up_to_date() -> bool:
     return _newer(LIB, _inputs())
 
 
+def _interpreter() -> str:
+    """The torch and Python that the binding's machine code has to fit."""
+    import torch
+
+    return f"torch {torch.__version__}, Python {sys.version}"
+
+
 def binding_up_to_date() -> bool:
+    try:
+        with open(BINDING_FOR) as f:
+            if f.read() != _interpreter():
+                return False
+    except FileNotFoundError:
+        return False
     return _newer(BINDING, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "mambascan.h"),
                             os.path.abspath(__file__)])
 
@@ -67,6 +81,9 @@ def build_binding(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(BINDING_FOR), exist_ok=True)
+    with open(BINDING_FOR, "w") as f:
+        f.write(_interpreter())
     return BINDING
 
 
