@@ -28,9 +28,7 @@ __all__ = [
     "load_library", "MambaScanError", "ScanArgs", "UpdateArgs", "ScanPlan", "MS_F32", "MS_BF16",
     "Conv1dArgs", "conv_scan_fwd", "conv_state_update", "build_conv_args", "trap_scan_fwd",
     "ScanBwdArgs", "scan_bwd", "SsdArgs", "build_ssd_args", "ssd_fwd", "ssd_check", "SSD_WORKSPACE_BYTES",
-    "ConvPackedArgs", "conv_packed_fwd", "conv_packed_update", "SsdUpdateArgs", "ssd_state_update",
-    "SsdPackedArgs", "ssd_packed_fwd",
-    "NormArgs", "NormBwdArgs", "norm_fwd", "norm_bwd",
+    "ConvPackedArgs", "SsdUpdateArgs", "SsdPackedArgs", "NormArgs", "NormBwdArgs",
     "MAX_DSTATE", "probe_unit_throughput", "PROBE_UNITS", "plan_workspace_size", "scan_status",
 ]
 
@@ -851,7 +849,9 @@ def ssd_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, init
 
 
 # ----------------------------------------------------------------------------
-# Mamba-2 serving operators and norms (serving.py, loaded with torch on first use)
+# Mamba-2 serving operators and norms: serving.py, which needs torch and the compiled
+# binding, so it is loaded when one of them is first asked for (and they are not in
+# __all__, whose names a star import asks for at once)
 
 _SERVING = ("conv_packed_fwd", "conv_packed_update", "ssd_packed_fwd", "ssd_state_update", "norm_fwd", "norm_bwd")
 
@@ -863,6 +863,10 @@ def __getattr__(name):
             globals()[n] = getattr(serving, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *_SERVING})
 
 
 PROBE_UNITS = {"ex2": 0, "tanh": 1, "ffma": 2, "ffma2": 3}
