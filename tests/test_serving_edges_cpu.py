@@ -6,6 +6,7 @@ import pytest
 import selective_state_space_27_b200 as ms
 from selective_state_space_27_b200 import build as msbuild
 from tests.test_serving_cpu import BASE, conv_args, conv_filter
+from tests.test_serving_edges_gpu import SCHEDULES
 
 
 @pytest.fixture(scope="module")
@@ -29,3 +30,13 @@ def test_conv_packed_refuses_overlapping_outputs(lib, change):
     """y that shares elements with x: its rows are written while x's are read again for later rows."""
     assert lib.mamba_conv_packed_fwd(ctypes.byref(conv_args(**change)), ctypes.byref(conv_filter()), None) == 1
     assert b"overlap" in lib.mamba_last_error()
+
+
+def test_schedules_of_these_sizes(lib):
+    """ms::ssd_packed_plan, which chooses a call's schedule from its sizes, on 148 SMs."""
+    plan = lib["_ZN2ms15ssd_packed_planEllllli"]
+    plan.restype, plan.argtypes = ctypes.c_int64, [ctypes.c_int64] * 5 + [ctypes.c_int]   # (two int32 in one register)
+    extra = 130 + 3                                          # rows of no sequence
+    for lens, heads, groups, *_, longest, schedule in SCHEDULES:
+        got = plan(sum(lens) + extra, len(lens), heads, groups, longest, 148)
+        assert (got & 0xFFFFFFFF, got >> 32) == schedule, (len(lens), heads)

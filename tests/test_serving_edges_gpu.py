@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from tests import serving_ref as ref
-from tests.test_serving_gpu import F64, UB, close, conv_tol, i32, normal, offsets, rng, ssd_close, ssd_inputs
+from tests.test_serving_gpu import (F64, UB, close, conv_tol, i32, normal, offsets, rng, ssd_close, ssd_inputs,
+                                     test_ssd_packed as _test_ssd_packed)
 
 pytestmark = pytest.mark.gpu
 
@@ -14,6 +15,36 @@ pytestmark = pytest.mark.gpu
 def ms():
     import selective_state_space_27_b200 as m
     return m
+
+
+# ---- the schedules of large batches ---------------------------------------------------
+
+SCHEDULES = [
+    # (chunks per segment, heads per CTA) on 148 SMs: test_schedules_of_these_sizes holds them to it
+    # lens, heads, groups, gate, slots, indices, resumed, longest, schedule
+    # two heads per CTA, whole sequences: ragged ends, empty ones, resumed and skipped ones
+    ([300, 77, 128, 5, 0, 200], 64, 1, True, 7, [6, 0, 3, -1, 1, 5], [True, False, True, True, True, False], 300, (0, 2)),
+    ([257, 1, 256, 129], 80, 2, False, 4, None, [False, True, True, False], 257, (0, 2)),
+    # an odd number of heads in a group: its last pair is one head
+    ([200, 130, 40, 1, 0, 90, 60], 45, 3, True, 9, [8, 1, 1, 3, 4, 9, 0], [True] * 7, 200, (0, 2)),
+    # more than 32 whole sequences, two heads per CTA (the last pair of nine is one head), and one
+    ([40 - i % 9 for i in range(40)], 9, 1, False, 41, list(range(40, 0, -1)), [i % 2 == 0 for i in range(40)], 40, (0, 2)),
+    ([(37 * i) % 150 for i in range(45)], 2, 1, True, 50, [i if i % 7 else -1 for i in range(45)],
+     [i % 3 == 0 for i in range(45)], 148, (0, 1)),
+    # two heads per CTA in segments of two, three, four and six chunks
+    ([3000], 24, 1, False, 1, None, [True], 3000, (2, 2)),
+    ([1500], 64, 2, True, 2, [1], [False], 1500, (4, 2)),
+    ([4000], 48, 1, False, 1, [0], [True], 4000, (6, 2)),
+    ([2500, 0, 300], 45, 3, True, 3, [2, 0, 1], [True, True, False], 2500, (3, 2)),
+    # one head per CTA in segments of three chunks
+    ([9000], 5, 1, False, 1, None, [True], 9000, (3, 1)),
+]
+
+
+@pytest.mark.parametrize("lens,H,G,gate,slots,idx,resumed,longest,schedule", SCHEDULES)
+def test_ssd_packed_schedules(ms, lens, H, G, gate, slots, idx, resumed, longest, schedule):
+    """The forms that large batches take, against the definition, rows of no sequence and skipped slots among them."""
+    _test_ssd_packed(ms, lens, H, G, gate, slots, idx, resumed, longest)
 
 
 # ---- NaN in the decay --------------------------------------------------------------
