@@ -1082,7 +1082,6 @@ ms_status mamba_norm_bwd(const ms_norm_args *a, const ms_norm_bwd_args *g, void 
     q.dres = g->dresidual; q.dres_sr = g->dresidual_row_stride;
     q.dw = g->dweight;
     q.slabs = slabs;
-    q.need_x = need_x;
     if (g->dweight) {
         if (slabs == 1) {
             q.partial = g->dweight;

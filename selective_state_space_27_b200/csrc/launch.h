@@ -257,7 +257,6 @@ struct NormBwdParams {
     float *dw;
     float *partial;           // (slabs, dim) shares of dw; dw itself for one slab; null without dw
     int64_t slabs;            // row slabs per group
-    int need_x;               // x is read (the branch enters the norm by itself, or has a gate)
 };
 // Slabs the backward takes for these sizes.
 int64_t norm_bwd_slabs(int64_t rows, int64_t dim, int64_t gs, int num_sms);

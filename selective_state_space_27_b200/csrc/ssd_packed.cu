@@ -1127,8 +1127,8 @@ constexpr double kOneHead = 0.7;
 // most c chunks take c when they all run at once, else their work spread over
 // the places plus half a CTA at the end. A CTA's start costs about 0.7 of a
 // chunk; a chunk of the first kernel costs half as much as one of the third,
-// and the additional launches and the pass along the segments about 1 and one
-// thousandth of a chunk for each segment and head.
+// the additional launches about 1, and the pass along the segments one
+// two-thousandth for each head and each segment but a sequence's last.
 SsdPackedPlan ssd_packed_plan(int64_t tokens, int64_t nseq, int64_t nheads, int64_t ngroups, int64_t max_seqlen, int num_sms)
 {
     const double slots = num_sms > 0 ? num_sms : 1;
