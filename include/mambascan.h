@@ -631,6 +631,7 @@ ms_status mamba_scan_fwd_noalloc(const ms_scan_args *args, void *stream);
  *           row strides given. Unused (NULL) when width is 1.
  * cu_seqlens NULL is the single-token form: tokens == nseq, sequence s is row s.
  * y must not overlap x, refused (a row is read again for the rows behind it and the state).
+ * Limits: tokens up to 2^31 - 65, channels up to 2^22, nseq up to 2^30.
  */
 typedef struct ms_conv_packed_args {
     int64_t tokens, channels, nseq, slots;
@@ -655,7 +656,10 @@ ms_status mamba_conv_packed_fwd(const ms_conv_packed_args *args, const ms_conv1d
  * x, y, z, B and C are 16-byte aligned with token strides that are multiples of
  * 8 elements. y may be x or z itself, but overlap no other input. max_seqlen: the
  * longest sequence as far as the host knows it (0: not known); it steers the
- * schedule only.
+ * schedule only. Up to 32 sequences that are not cut run longest first, more in the
+ * caller's order: a long one is best not the last. Limits: tokens below 2^31 -
+ * 2^16, nheads up to 65535, nseq nheads up to 2^27, (tokens / 256 + nseq) nheads
+ * below 2^31.
  */
 typedef struct ms_ssd_packed_args {
     int64_t tokens, nseq, nheads, ngroups, slots, max_seqlen;
@@ -716,7 +720,8 @@ ms_status mamba_ssd_packed_failures(uint64_t *count, void *stream);
  *   state   : (slots, nheads, headdim, dstate) float32, updated in place; slot
  *             stride given, inner axes contiguous
  * Any headdim up to 65535, dstate up to MS_SSD_UPDATE_MAX_DSTATE; in_dtype f32
- * or bf16. y may be x or z itself, but overlap no other input.
+ * or bf16. y may be x or z itself, but overlap no other input. Limits: batch and
+ * nheads up to 65535, nheads headdim up to 2^30.
  */
 #define MS_SSD_UPDATE_MAX_DSTATE 256
 typedef struct ms_ssd_update_args {
@@ -748,7 +753,8 @@ ms_status mamba_ssd_state_update(const ms_ssd_update_args *args, void *stream);
  * (z, groups). x, z, y, dy: in_dtype; residual and residual_out:
  * residual_dtype, which is in_dtype or MS_F32. Row strides given, channels
  * contiguous. weight: (dim) float32. y may be x or z itself, and residual_out
- * residual; the outputs overlap no other input.
+ * residual; the outputs overlap no other input. Limits: dim up to 2^30, rows times
+ * groups below 2^31.
  */
 typedef struct ms_norm_args {
     int64_t rows, dim, group_size;

@@ -16,7 +16,9 @@
 // of 64 (28 warps per SM fit instead of 32). Measured before the rows waited in
 // shared memory: eight channels per thread 117 us (too few warps), two 89 us,
 // eight tiles per thread instead of one stretch of rows 104 us. The special
-// function unit is 59% busy (exponential and reciprocal of the SiLU).
+// function unit is 64% busy (exponential and reciprocal of the SiLU). float32: 154
+// us (83%). 4353 channels, one per thread without rows ahead in shared
+// memory: 156 us in bf16, 208 in float32.
 //
 // Two kinds of work. A tile is a stretch of consecutive rows of the packed
 // stream, whatever sequences they belong to, except each sequence's first

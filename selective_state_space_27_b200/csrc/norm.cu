@@ -15,12 +15,16 @@
 // its slab, so that its share of dw stays in registers; the slabs' shares are
 // added by a second kernel.
 // Measured on B200 for 16384 rows x 8 groups of 512, bf16, gated: forward 73 us
-// (84% of the measured copy bandwidth), backward 127 us (81%). 128 registers leave
+// (84% of the measured copy bandwidth), backward 125 us (82%; 130 to 135 over
+// seconds, where the clock falls under the power limit). 116 registers leave
 // the backward 16 warps per SM: with a row's loads in registers they came in bursts
 // between the reductions (137 us), so the next rows wait in shared memory, and the
 // row in work is read from there twice (once, held over the reduction: 130 us).
-// 4099 rows x 1530, float32, with a residual: backward 31 us (62%, 6 us of it the
-// second kernel's). The same for the forward (teams walk rows, the next ones in
+// 4099 rows x 1530, float32, with a residual: backward 31 us (62%, 5 us of it the
+// second kernel's). 16384 x 2048, bf16, float32 residual: 66 us (93%), backward 130
+// us (63%). bf16 groups that are no multiple of 8 take vectors of two or one element
+// without the usual modes: 16384 x 8 groups of 500, gated, 119 and 267 us; 16384 x
+// 5001, two passes by single elements, 316 us and 1.01 ms. The same for the forward (teams walk rows, the next ones in
 // shared memory) gave 72 to 76 us against 73. Taking the gate's two reciprocals of a pair from one of their
 // product, to relieve the special function unit (56% busy in the forward), made
 // all of them slower: 86 and 158 us.

@@ -30,8 +30,9 @@
 // the next state. The decayed state and the decayed inter-chunk term with the
 // skip are written into the accumulators, so the products add onto them.
 // Roles (640 threads): warps 0-15 arithmetic (head w / 8; rows 32 (w % 4) ..
-// + 31 of the tile; columns by half, sixteen at a time: nothing may spill, the
-// L1 that shared memory leaves is too small for it), warps 16-17 the heads' step
+// + 31 of the tile; columns by half, sixteen at a time: next to nothing may spill
+// (three registers of the gated kernel do), the L1 that shared memory leaves is too
+// small for it), warps 16-17 the heads' step
 // sizes, warp 18 TMA loads, warp 19 tensor memory and MMA issue.
 // Order within a chunk: w X while G and C H^T run; the start of Y; M' while the
 // state product runs; the next state while M' X runs. Loads go out as soon as
@@ -45,17 +46,18 @@
 // on the stream, each starting while the one in front of it ends; no CTA waits
 // for another one of its kernel.
 //
-// Measured on B200, bf16: 16 ragged prompts of 24000 tokens, 64 heads, half of
-// them resumed, 182 us (38% of the time its bytes take; the longest prompts first,
-// so the SMs end within 3% of each other); 4 x 8192 tokens x 64 heads 237 us (the
-// dense kernel, one head per CTA: 385 us); one prompt of 32768 tokens x 24 heads
-// 135 us in segments, 40 + 8 + 95 us one by one; three prompts of 378 tokens x 24
-// heads 11 us on the device, 14 with two heads per CTA. A chunk of a pair of heads takes about 6800 clocks, of
+// Measured on B200, bf16, in runs of a few milliseconds: 16 ragged prompts of 24000
+// tokens, 64 heads, half of them resumed, 183 us (2.6 times what its bytes take; the
+// longest prompts first, so the SMs end within 3% of each other); 4 x 8192 tokens x
+// 64 heads 239 us (the dense kernel, one head per CTA: 385 us); one prompt of 32768
+// tokens x 24 heads 136 to 142 us in segments, 41 + 8 + 99 us one by one. Over
+// seconds the clock falls under the power limit: 203, 260 and 142 us. Three prompts
+// of 378 tokens x 24 heads take 13 us on the device in a chain of calls. A chunk of a pair of heads takes about 6800 clocks, of
 // which the tensor core works 45%. What bounds it is the chain w X - state
 // product - next state - C H^T together with shared memory, which is about 75%
 // busy with the products' operands (2304 clocks), TMA (1024) and the arithmetic
 // warps' own accesses (1800), so that arithmetic beside the products slows both.
-// Measured and not kept (4 x 8192 x 64 heads, against 240 us): C H^T issued before
+// Measured and not kept (4 x 8192 x 64 heads, against 240 us at the time): C H^T issued before
 // G 259 us; w X made while M' X runs 249 us; X kept in registers 241 us (spills);
 // one head per CTA and two CTAs per SM 298 us; w X shared out unevenly 271 us; M'
 // made while C H^T runs and the next hi term beside M' X (X then read twice) 255 us.
@@ -206,6 +208,8 @@ struct Segment {
 // before the next one's first place; places in between have nothing to do.
 // Up to 32 sequences are looked up together, one per lane, with their slots and
 // in one round of loads (a CTA starts with it); more are searched 32 at a time.
+// Whole sequences run longest first up to 32, else in the caller's order (39 of 300
+// tokens and one of 1500, 64 heads: 153 us with the long one first, 174 us last).
 // slot: the sequence's cache slot, -1 when it is skipped. Called by whole blocks.
 __device__ __forceinline__ bool find_segment(const SsdPackedParams &p, int64_t place, int lane, Segment &g, int &slot)
 {
