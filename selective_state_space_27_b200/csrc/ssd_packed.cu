@@ -52,13 +52,14 @@
 // 64 heads 239 us (the dense kernel, one head per CTA: 385 us); one prompt of 32768
 // tokens x 24 heads 136 to 142 us in segments, 41 + 8 + 99 us one by one. Over
 // seconds the clock falls under the power limit: 203, 260 and 142 us. Three prompts
-// of 378 tokens x 24 heads take 13 us on the device in a chain of calls. A chunk of a pair of heads takes about 6800 clocks, of
+// of 378 tokens x 24 heads take 13 us on the device in a chain of calls.
+// A chunk of a pair of heads takes about 6800 clocks, of
 // which the tensor core works 45%. What bounds it is the chain w X - state
 // product - next state - C H^T together with shared memory, which is about 75%
 // busy with the products' operands (2304 clocks), TMA (1024) and the arithmetic
 // warps' own accesses (1800), so that arithmetic beside the products slows both.
-// Measured and not kept (4 x 8192 x 64 heads, against 240 us at the time): C H^T issued before
-// G 259 us; w X made while M' X runs 249 us; X kept in registers 241 us (spills);
+// Measured and not kept (4 x 8192 x 64 heads, against 240 us at the time): C H^T
+// issued before G 259 us; w X made while M' X runs 249 us; X kept in registers 241 us (spills);
 // one head per CTA and two CTAs per SM 298 us; w X shared out unevenly 271 us; M'
 // made while C H^T runs and the next hi term beside M' X (X then read twice) 255 us.
 #include <cuda.h>

@@ -216,10 +216,11 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
     every sequence starts from zero and leaves no state). ``max_seqlen``: the
     longest sequence if the host knows it; it steers the schedule only.
     Returns y (tokens, nheads, 64); rows of no or of a skipped sequence are not
-    written. ``out`` may be x or z itself, but overlap no other input, nor them in part. ``workspace``: a uint8 CUDA tensor, allocated here when None. With
-    ``check`` the call synchronizes the stream and raises if the kernel
-    reported a failed wait (a workspace that is too small is then replaced);
-    without it, pass a workspace and call :func:`ssd_check` on it later (one
+    written. ``out`` may be x or z itself, but overlap no other input, nor them
+    in part. ``workspace``: a uint8 CUDA tensor, allocated here when None. With
+    ``check`` the call synchronizes the stream (so it cannot be captured) and
+    raises if the kernel reported a failed wait (a workspace that is too small
+    is then replaced); without it, pass a workspace and call :func:`ssd_check` on it later (one
     that is too small is refused: the status would not be in it), or call
     ``ssd_check()`` after a number of calls without one.
     """
