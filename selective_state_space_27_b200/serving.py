@@ -220,9 +220,9 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
     in part. ``workspace``: a uint8 CUDA tensor, allocated here when None. With
     ``check`` the call synchronizes the stream (so it cannot be captured) and
     raises if the kernel reported a failed wait (a workspace that is too small
-    is then replaced); without it, pass a workspace and call :func:`ssd_check` on it later (one
-    that is too small is refused: the status would not be in it), or call
-    ``ssd_check()`` after a number of calls without one.
+    is then replaced); without it, pass a workspace and call :func:`ssd_check`
+    on it later (one that is too small is refused: the status would not be in
+    it), or call ``ssd_check()`` after a number of calls without one.
     """
     if stream is not None:
         return _given(stream, x, ssd_packed_fwd, locals())
